@@ -267,6 +267,133 @@ HS2_API hs2_status hs2_kv_quantize_fp8(const float* src, int64_t rows, int32_t h
                                float* scales, hs2_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Around the block: rows for the cache, layers with a sliding window, and a
+ * cache of bounded size.  The pages name the parts (the compulsory window of the
+ * latest 128 tokens; the Hybrid-SWA layers HySparse2 is compared with; caches
+ * that must stay small) and give no formulas; the formulas below are this
+ * library's.  Conventions as above, and for these four calls:
+ *   - n_rows is an optional device int32 array [batch]: sequence b uses rows
+ *     0 .. n_rows[b] - 1 of its n (n_q) rows (a padded batch; values are clamped
+ *     to [0, n]); the other rows are neither read nor written.  NULL: all rows.
+ *   - heads is 1 .. 128 and head_dim 64 or 128 for every type.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Description of hs2_qk_norm_rope; plain data, read by the callee and not retained. */
+typedef struct {
+    int32_t batch;          /* sequences                                             */
+    int32_t n;              /* rows per sequence                                     */
+    int32_t heads;          /* query heads                                           */
+    int32_t head_dim;       /* 64 or 128                                             */
+    int32_t rot_dim;        /* leading dims of a head that rotate: 0, 16, 32 .. head_dim */
+    int32_t interleaved;    /* 0: pairs (i, i + rot_dim/2); else pairs (2i, 2i + 1)  */
+    int32_t normalize;      /* 0: no norm (weights and eps unused)                   */
+    int32_t in_dtype;       /* HS2_F32 or HS2_BF16: q, k, v and q_out                */
+    int32_t kv_dtype;       /* the cache: HS2_F32 (f32 rows only), HS2_BF16, HS2_E4M3 */
+    float   eps;            /* added to the mean square, >= 0                        */
+    int64_t q_row;          /* elements from row t to t + 1 of q, k, v (multiples of */
+    int64_t k_row;          /* 16 bytes; a sequence's rows follow the one before's:  */
+    int64_t v_row;          /* element stride n * row between sequences)             */
+    int64_t kv_capacity;    /* cache rows per sequence                               */
+} hs2_rope_desc;
+
+/*
+ * Norm of each query head and of the key, position rotation, and the write of the
+ * key and value rows to the cache, in one pass.  For a head x of row t:
+ *   y   = x * rsqrt(mean(x^2) + eps) * weight            (normalize != 0)
+ *   (a, b) -> (a cos - b sin, b cos + a sin) for its pairs i, the angle being
+ *         pos[b][t] * inv_freq[i], reduced in fp64
+ * q [batch][n] rows of heads * head_dim values, k and v rows of head_dim values, so
+ * that the three may be slices of one fused projection.  Rotated queries go to q_out
+ * [batch][n][heads][head_dim]; the rotated key and the unchanged value go to cache
+ * rows row0[b] + t of k_cache, v_cache in kv_dtype (E4M3: quantized per row exactly as
+ * hs2_kv_quantize_fp8 does it, scales to k_scale, v_scale).  A row outside the cache
+ * is not written.  Arithmetic is fp32, rounded once on the way out.
+ *   q, k, v        any of them may be NULL: that part is left out (k_cache etc. are
+ *                  then unused, q_out with q)
+ *   q_weight, k_weight  optional [head_dim] fp32 (NULL: 1)
+ *   inv_freq       [rot_dim / 2] fp64, radians per position (may be NULL if rot_dim is 0)
+ *   row0           device int32 [batch]
+ *   pos            optional device int32 [batch][n]; NULL: position = cache row
+ *   q_out          may be q itself where q_row = heads * head_dim; otherwise no output
+ *                  overlaps an input
+ * No workspace.
+ */
+HS2_API hs2_status hs2_qk_norm_rope(const hs2_rope_desc* desc, const void* q, const void* k, const void* v,
+                                    const float* q_weight, const float* k_weight, const double* inv_freq,
+                                    const int32_t* row0, const int32_t* pos, const int32_t* n_rows, void* q_out,
+                                    void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                    hs2_stream_t stream);
+
+/* Workspace bytes of hs2_window_attn (0 for an invalid description). */
+HS2_API size_t hs2_window_workspace_size(const hs2_attn_desc* desc, int32_t sinks);
+
+/*
+ * Attention layer with a sliding window and sinks: the query at position p attends
+ * to the cache rows j <= p with j > p - desc->window or j < sinks (a row in both
+ * counts once), sinks >= 0.  o = softmax(softmax_scale q k^T) v over those rows,
+ * lse (optional) the log of the sum.  Serves single tokens (n_q = 1) and chunks.
+ * desc->budget and idx_stride are not used.  Cache rows that no query of the call
+ * attends to may hold anything; the rows that some query attends to must be finite.
+ * A query position outside [0, max_ctx) is clamped into it and reported as
+ * HS2_ERR_INDEX.
+ */
+HS2_API hs2_status hs2_window_attn(const hs2_attn_desc* desc, int32_t sinks, const void* q, const void* k,
+                                   const void* v, const float* k_scale, const float* v_scale,
+                                   const int32_t* q_pos0, const int32_t* n_rows, void* o, float* lse,
+                                   void* workspace, size_t ws_bytes, hs2_stream_t stream);
+
+/* Workspace bytes of hs2_weight_accum (0 for an invalid description). */
+HS2_API size_t hs2_weight_accum_workspace_size(const hs2_attn_desc* desc);
+
+/*
+ * Accumulated attention weight of the cached keys:
+ *   acc_out[b][j] = decay * acc_in[b][j] + sum over rows r and heads h of
+ *                   exp(softmax_scale q_rh . k_j - lse_rh)     [j <= q_pos0[b] + r]
+ * for the rows j < q_pos0[b] + n_rows[b]; acc_out's other entries are left as they
+ * were.  q and lse are a full-attention call's query and its lse output (the last
+ * rows of a prompt alone, or one new token, are ordinary uses).  acc_in, acc_out:
+ * [batch][kv_capacity] fp32; acc_in may be acc_out, or NULL for zeros (decay is then
+ * unused); decay >= 0.  desc->window, budget and idx_stride are not used.  The sums'
+ * order is fixed by the sizes: equal calls give equal bits.
+ */
+HS2_API hs2_status hs2_weight_accum(const hs2_attn_desc* desc, const void* q, const void* k,
+                                    const float* k_scale, const float* lse, const int32_t* q_pos0,
+                                    const int32_t* n_rows, float decay, const float* acc_in, float* acc_out,
+                                    void* workspace, size_t ws_bytes, hs2_stream_t stream);
+
+/* Description of hs2_kv_evict; plain data, read by the callee and not retained. */
+typedef struct {
+    int32_t batch;          /* sequences                                             */
+    int32_t head_dim;       /* 64 or 128                                             */
+    int32_t kv_dtype;       /* HS2_F32, HS2_BF16 or HS2_E4M3                         */
+    int32_t sinks;          /* first rows, always kept, >= 0                         */
+    int32_t window;         /* latest rows, always kept, >= 0                        */
+    int32_t budget;         /* other rows kept, >= 0                                 */
+    int64_t kv_capacity;    /* rows per sequence of the cache (and of acc)           */
+    int64_t out_capacity;   /* rows per sequence of the outputs,
+                               >= sinks + window + budget >= 1                       */
+} hs2_evict_desc;
+
+/*
+ * Eviction: of the len[b] rows of sequence b the first `sinks`, the latest `window`
+ * and the `budget` rows with the largest acc of those between them are kept (ties to
+ * the lower row; -0 equals 0 and a NaN ranks below every number), in their order, as
+ * rows 0 .. new_len[b] - 1 of k_out, v_out (and k_scale_out, v_scale_out for E4M3
+ * caches) and acc_out; new_len[b] = min(len[b], sinks + window + budget), all rows if
+ * they fit.  idx [batch][sinks + window + budget] int32 receives the kept rows,
+ * ascending, then -1.  Output rows from new_len[b] on are left as they were.
+ *   len      device int32 [batch], clamped to [0, kv_capacity]
+ *   acc      [batch][kv_capacity] fp32; acc_out optional [batch][out_capacity]
+ * Outputs must not overlap inputs.  No workspace.
+ */
+HS2_API hs2_status hs2_kv_evict(const hs2_evict_desc* desc, const int32_t* len, const float* acc, const void* k,
+                                const void* v, const float* k_scale, const float* v_scale, void* k_out,
+                                void* v_out, float* k_scale_out, float* v_scale_out, float* acc_out,
+                                int32_t* idx, int32_t* new_len, hs2_stream_t stream);
+
+/*
  * Waits for `stream`, reads and clears the device status word kept at the start
  * of `workspace`, and returns it (HS2_OK, HS2_ERR_TIMEOUT or HS2_ERR_INDEX), or
  * HS2_ERR_CUDA if the stream reported an error.

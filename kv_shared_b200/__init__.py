@@ -21,7 +21,8 @@ HS2_OK, HS2_ERR_INVALID_ARG, HS2_ERR_UNSUPPORTED, HS2_ERR_WORKSPACE, HS2_ERR_CUD
 EXPORTS = ("hs2_workspace_size", "hs2_workspace_init", "hs2_full_attn_select", "hs2_full_attn_launches",
            "hs2_topk_select",
            "hs2_sparse_attn", "hs2_sparse_attn_noalloc", "hs2_kv_bridge_proj", "hs2_kv_quantize_fp8", "hs2_last_status",
-           "hs2_status_string")
+           "hs2_status_string", "hs2_qk_norm_rope", "hs2_window_workspace_size", "hs2_window_attn",
+           "hs2_weight_accum_workspace_size", "hs2_weight_accum", "hs2_kv_evict")
 
 
 class hs2_attn_desc(ctypes.Structure):
@@ -30,6 +31,17 @@ class hs2_attn_desc(ctypes.Structure):
                 ("q_dtype", ctypes.c_int32), ("kv_dtype", ctypes.c_int32),
                 ("softmax_scale", ctypes.c_float), ("idx_stride", ctypes.c_int32),
                 ("kv_capacity", ctypes.c_int64), ("max_ctx", ctypes.c_int64)]
+
+
+class hs2_rope_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "n", "heads", "head_dim", "rot_dim", "interleaved",
+                                              "normalize", "in_dtype", "kv_dtype")] + \
+        [("eps", ctypes.c_float)] + [(n, ctypes.c_int64) for n in ("q_row", "k_row", "v_row", "kv_capacity")]
+
+
+class hs2_evict_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "head_dim", "kv_dtype", "sinks", "window", "budget")] + \
+        [("kv_capacity", ctypes.c_int64), ("out_capacity", ctypes.c_int64)]
 
 
 class HS2Error(RuntimeError):
@@ -63,8 +75,17 @@ def lib():
         L.hs2_last_status.argtypes = [vp, vp]
         L.hs2_status_string.argtypes = [ctypes.c_int]
         L.hs2_status_string.restype = ctypes.c_char_p
+        rp, ep, f32 = ctypes.POINTER(hs2_rope_desc), ctypes.POINTER(hs2_evict_desc), ctypes.c_float
+        L.hs2_qk_norm_rope.argtypes = [rp] + [vp] * 15
+        L.hs2_window_workspace_size.argtypes = [dp, i32]
+        L.hs2_window_workspace_size.restype = sz
+        L.hs2_window_attn.argtypes = [dp, i32] + [vp] * 10 + [sz, vp]
+        L.hs2_weight_accum_workspace_size.argtypes = [dp]
+        L.hs2_weight_accum_workspace_size.restype = sz
+        L.hs2_weight_accum.argtypes = [dp] + [vp] * 6 + [f32] + [vp] * 3 + [sz, vp]
+        L.hs2_kv_evict.argtypes = [ep] + [vp] * 14
         for name in EXPORTS:
-            if name not in ("hs2_workspace_size", "hs2_status_string"):
+            if not name.endswith("workspace_size") and name != "hs2_status_string":
                 getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -158,20 +179,95 @@ def hs2_kv_quantize_fp8(src, rows, head_dim, codes, scales, stream=None):
     _check("hs2_kv_quantize_fp8", st)
 
 
+def make_rope_desc(batch, n, heads, head_dim, rot_dim=None, interleaved=False, normalize=True, in_dtype=HS2_BF16,
+                   kv_dtype=HS2_BF16, eps=1e-6, q_row=None, k_row=None, v_row=None, kv_capacity=None):
+    d = hs2_rope_desc()
+    d.batch, d.n, d.heads, d.head_dim = batch, n, heads, head_dim
+    d.rot_dim = head_dim if rot_dim is None else rot_dim
+    d.interleaved, d.normalize = int(bool(interleaved)), int(bool(normalize))
+    d.in_dtype, d.kv_dtype, d.eps = in_dtype, kv_dtype, eps
+    d.q_row = heads * head_dim if q_row is None else q_row
+    d.k_row = head_dim if k_row is None else k_row
+    d.v_row = head_dim if v_row is None else v_row
+    d.kv_capacity = n if kv_capacity is None else kv_capacity
+    return d
+
+
+def make_evict_desc(batch, head_dim, kv_dtype=HS2_BF16, sinks=0, window=128, budget=1024, kv_capacity=None,
+                    out_capacity=None):
+    d = hs2_evict_desc()
+    d.batch, d.head_dim, d.kv_dtype = batch, head_dim, kv_dtype
+    d.sinks, d.window, d.budget = sinks, window, budget
+    d.kv_capacity = kv_capacity
+    d.out_capacity = sinks + window + budget if out_capacity is None else out_capacity
+    return d
+
+
+def hs2_qk_norm_rope(desc, q, k, v, q_weight, k_weight, inv_freq, row0, pos, n_rows, q_out, k_cache, v_cache,
+                     k_scale=None, v_scale=None, stream=None):
+    st = lib().hs2_qk_norm_rope(ctypes.byref(desc), _p(q), _p(k), _p(v), _p(q_weight), _p(k_weight), _p(inv_freq),
+                                _p(row0), _p(pos), _p(n_rows), _p(q_out), _p(k_cache), _p(v_cache), _p(k_scale),
+                                _p(v_scale), _stream(stream))
+    _check("hs2_qk_norm_rope", st)
+
+
+def hs2_window_workspace_size(desc, sinks=0):
+    return int(lib().hs2_window_workspace_size(ctypes.byref(desc), int(sinks)))
+
+
+def hs2_window_attn(desc, sinks, q, k, v, k_scale, v_scale, q_pos0, n_rows, o, lse, workspace, stream=None):
+    st = lib().hs2_window_attn(ctypes.byref(desc), int(sinks), _p(q), _p(k), _p(v), _p(k_scale), _p(v_scale),
+                               _p(q_pos0), _p(n_rows), _p(o), _p(lse), _p(workspace),
+                               workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("hs2_window_attn", st)
+
+
+def hs2_weight_accum_workspace_size(desc):
+    return int(lib().hs2_weight_accum_workspace_size(ctypes.byref(desc)))
+
+
+def hs2_weight_accum(desc, q, k, k_scale, lse, q_pos0, n_rows, decay, acc_in, acc_out, workspace, stream=None):
+    st = lib().hs2_weight_accum(ctypes.byref(desc), _p(q), _p(k), _p(k_scale), _p(lse), _p(q_pos0), _p(n_rows),
+                                float(decay), _p(acc_in), _p(acc_out), _p(workspace),
+                                workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("hs2_weight_accum", st)
+
+
+def hs2_kv_evict(desc, len_, acc, k, v, k_scale, v_scale, k_out, v_out, k_scale_out, v_scale_out, acc_out, idx,
+                 new_len, stream=None):
+    st = lib().hs2_kv_evict(ctypes.byref(desc), _p(len_), _p(acc), _p(k), _p(v), _p(k_scale), _p(v_scale), _p(k_out),
+                            _p(v_out), _p(k_scale_out), _p(v_scale_out), _p(acc_out), _p(idx), _p(new_len),
+                            _stream(stream))
+    _check("hs2_kv_evict", st)
+
+
 def hs2_last_status(workspace, stream=None):
     """Waits for the stream and returns (and clears) the device status word."""
     return int(lib().hs2_last_status(_p(workspace), _stream(stream)))
 
 
 # ------------------------------------------------------------------ allocation helpers (plumbing)
-def alloc_workspace(desc, scores_in_workspace=True, device="cuda"):
-    n = hs2_workspace_size(desc, scores_in_workspace)
+def _alloc(fn, n, device):
     if n == 0:
-        raise HS2Error("hs2_workspace_size", HS2_ERR_INVALID_ARG)
+        raise HS2Error(fn, HS2_ERR_INVALID_ARG)
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     hs2_workspace_init(ws)
     return ws
 
 
-__all__ = ["hs2_attn_desc", "HS2Error", "make_desc", "lib", "status_string", "alloc_workspace",
+def alloc_workspace(desc, scores_in_workspace=True, device="cuda"):
+    return _alloc("hs2_workspace_size", hs2_workspace_size(desc, scores_in_workspace), device)
+
+
+def alloc_window_workspace(desc, sinks=0, device="cuda"):
+    return _alloc("hs2_window_workspace_size", hs2_window_workspace_size(desc, sinks), device)
+
+
+def alloc_accum_workspace(desc, device="cuda"):
+    return _alloc("hs2_weight_accum_workspace_size", hs2_weight_accum_workspace_size(desc), device)
+
+
+__all__ = ["hs2_attn_desc", "hs2_rope_desc", "hs2_evict_desc", "HS2Error", "make_desc", "make_rope_desc",
+           "make_evict_desc", "lib", "status_string", "alloc_workspace", "alloc_window_workspace",
+           "alloc_accum_workspace",
            "HS2_F32", "HS2_BF16", "HS2_E4M3", "EXPORTS"] + list(EXPORTS)

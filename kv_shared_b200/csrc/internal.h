@@ -235,4 +235,101 @@ cudaError_t launch_bridge(const BridgeArgs& a, cudaStream_t st);
 cudaError_t launch_fp8_quantize(const float* src, int64_t rows, int head_dim, uint8_t* codes,
                                 float* scales, cudaStream_t st);
 
+// ---------------------------------------------------------------- rows for the cache
+struct RopeArgs {
+    int batch, n, heads, head_dim, rot;
+    bool interleaved, normalize, in_f32;
+    int kv_dtype;
+    float eps;
+    int64_t q_row, k_row, v_row, cap;
+    const void* q;           // rows of heads * head_dim values, q_row apart (or null)
+    const void* k;
+    const void* v;
+    const float* q_weight;   // [head_dim] or null
+    const float* k_weight;
+    const double* inv_freq;  // [rot / 2]
+    const int32_t* row0;     // [batch]
+    const int32_t* pos;      // [batch][n] or null
+    const int32_t* n_rows;   // [batch] or null
+    void* q_out;
+    void* k_cache;
+    void* v_cache;
+    float* k_scale;
+    float* v_scale;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st);
+
+// ---------------------------------------------------------------- sliding window
+// Keys of a tile of consecutive query rows as one list: the sinks outside the window's
+// range (padded to a multiple of kSinkPad), then the rows from the first row's window
+// start to the last row's position.
+constexpr int kSinkPad = 16;
+struct WindowArgs {
+    int batch, n_q, heads, head_dim, window, sinks;
+    int64_t cap, max_ctx;
+    const int32_t* q_pos0;
+    const int32_t* n_rows;   // [batch] or null
+    const void* q;           // [B][n_q][H][D] f32 or bf16
+    const void* k;           // [B][cap][D] f32, bf16 or e4m3
+    const void* v;
+    const float* k_scale;    // [B][cap] (e4m3)
+    const float* v_scale;
+    int kv_dtype;
+    float scale;
+    void* o;                 // [B][n_q][H][D] in q's type
+    float* lse;              // [B][n_q][H] or null
+    float* part_o;           // splits > 1: [split][B * n_q * H][D] unnormalised O
+    float2* part_ml;         //             [split][B * n_q * H] (max, sum) in log2 units
+    int splits;
+    uint32_t* status;
+};
+struct WindowPlan {
+    int splits;              // parts the keys of each tile are cut into
+};
+WindowPlan plan_window(int batch, int n_q, int heads, int kv_dtype, int window, int sinks, int64_t max_ctx);
+size_t window_ws_bytes(int batch, int n_q, int heads, int head_dim, int splits);
+cudaError_t launch_window(const WindowArgs& a, cudaStream_t st);
+
+// ---------------------------------------------------------------- accumulated weight
+struct AccumArgs {
+    int batch, n_q, heads, head_dim;
+    int64_t cap, max_ctx;
+    const int32_t* q_pos0;
+    const int32_t* n_rows;   // [batch] or null
+    const void* q;           // [B][n_q][H][D]
+    const void* k;           // [B][cap][D]
+    const float* k_scale;
+    int kv_dtype;
+    const float* lse;        // [B][n_q][H] natural log
+    float scale, decay;
+    const float* acc_in;     // [B][cap] or null
+    float* acc_out;          // [B][cap]
+    float* part;             // splits > 1: [split][B][max_ctx]
+    int splits;              // parts the query rows are cut into
+    uint32_t* status;
+};
+int plan_accum(int batch, int n_q, int heads, int kv_dtype, int64_t max_ctx);
+size_t accum_ws_bytes(int batch, int splits, int64_t max_ctx);
+cudaError_t launch_accum(const AccumArgs& a, cudaStream_t st);
+
+// ---------------------------------------------------------------- eviction
+struct EvictArgs {
+    int batch, head_dim, kv_dtype, sinks, window, budget;
+    int64_t cap, out_cap;
+    const int32_t* len;
+    const float* acc;        // [B][cap]
+    const void* k;
+    const void* v;
+    const float* k_scale;
+    const float* v_scale;
+    void* k_out;
+    void* v_out;
+    float* k_scale_out;
+    float* v_scale_out;
+    float* acc_out;          // [B][out_cap] or null
+    int32_t* idx;            // [B][sinks + window + budget]
+    int32_t* new_len;        // [B]
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st);
+
 }  // namespace hs2

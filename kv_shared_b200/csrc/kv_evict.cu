@@ -1,0 +1,276 @@
+// kv_evict.cu -- eviction from a cache by accumulated attention weight.
+//
+// Of a sequence's n rows the first `sinks`, the latest `window` and the `budget` largest
+// totals between them survive, in order.  Two launches:
+//
+//   select  one cluster of CTAs per sequence.  The totals' bit patterns, made to order like
+//           the values, are cut by three rounds of 11, 11 and 10 bits: each CTA counts its
+//           slice into shared memory, the cluster adds the counts, and the round's digit is
+//           the one in which the budget runs out.  The exact threshold pattern T and how
+//           many equal to it are still wanted (the lowest rows) follow; a last pass counts
+//           per warp and writes the survivors' rows in order, with no atomics on the output
+//           positions, so that equal calls give equal bits.
+//   move    one warp per few rows copies K, V, scales and totals to their new places.
+//
+// Bound by HBM: 4 bytes per row of the totals (read once from HBM, then from L2) and twice
+// the surviving rows' bytes.
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace hs2 {
+namespace {
+
+constexpr int ST = 1024;                         // threads of a select CTA
+constexpr int SW = ST / 32;
+constexpr int BINS = 2048;
+constexpr int LD = 8;                            // totals in flight per lane
+
+// Bits that order like the values: -0 as 0, a NaN below everything.
+__device__ __forceinline__ uint32_t order_bits(float x) {
+    if (x != x) return 0u;
+    const uint32_t u = __float_as_uint(x + 0.f);                // -0 + 0 = 0
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// A lane's LD totals 32 apart from position i on (0 from `end` on).
+__device__ __forceinline__ void load_part(const float* acc, int i, int end, float (&x)[LD]) {
+#pragma unroll
+    for (int j = 0; j < LD; ++j) x[j] = i + 32 * j < end ? __ldg(acc + i + 32 * j) : 0.f;
+}
+
+// Sum over the threads before this one; *total: over all (ST threads; scratch [SW + 1]).
+__device__ __forceinline__ int block_scan(int v, int* scratch, int* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();                                            // scratch is free
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int w = scratch[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        scratch[lane] = w;
+    }
+    __syncthreads();
+    *total = scratch[SW - 1];
+    return x - v + (warp ? scratch[warp - 1] : 0);
+}
+
+__global__ void __launch_bounds__(ST) evict_select_kernel(EvictArgs a) {
+    cg::cluster_group cluster = cg::this_cluster();
+    const int cs = static_cast<int>(cluster.num_blocks()), cr = static_cast<int>(cluster.block_rank());
+    const int b = blockIdx.x / cs;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ int hist[BINS], sums[BINS];
+    __shared__ int scratch[SW + 1];
+    __shared__ int digit, rest, count2[2];
+    __shared__ int before2[2];
+
+    const int64_t keep = static_cast<int64_t>(a.sinks) + a.window + a.budget;
+    int64_t n64 = a.len[b];
+    n64 = n64 < 0 ? 0 : (n64 > a.cap ? a.cap : n64);
+    const int n = static_cast<int>(n64);
+    const int kept = n < keep ? n : static_cast<int>(keep);
+    int32_t* idx = a.idx + b * keep;
+    if (cr == 0 && tid == 0) a.new_len[b] = kept;
+    for (int64_t i = kept + cr * ST + tid; i < keep; i += cs * ST) idx[i] = -1;
+    if (n <= keep) {                                            // the whole cluster takes this branch
+        for (int i = cr * ST + tid; i < n; i += cs * ST) idx[i] = i;
+        return;
+    }
+    const int first = a.sinks, m = n - a.window - a.sinks;      // candidates first .. first + m - 1, m > budget
+    for (int i = cr * ST + tid; i < a.sinks; i += cs * ST) idx[i] = i;
+    for (int i = cr * ST + tid; i < a.window; i += cs * ST) idx[a.sinks + a.budget + i] = n - a.window + i;
+    if (a.budget == 0) return;
+
+    // this CTA's slice of the candidates, and each warp's part of it
+    const int per = (m + cs - 1) / cs;
+    const int lo = min(m, cr * per), hi = min(m, lo + per);
+    const int seg = ((hi - lo + SW - 1) / SW + 31) & ~31;       // whole warps wide
+    const int s0 = min(hi, lo + warp * seg), s1 = min(hi, s0 + seg);
+    const float* acc = a.acc + b * a.cap + first;
+
+    uint32_t prefix = 0;                                        // bits of T found so far
+    int want = a.budget;                                        // still wanted among those that share them
+#pragma unroll 1
+    for (int round = 0; round < 3; ++round) {
+        const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0);
+        const uint32_t mask = round == 2 ? 1023u : 2047u;
+        const uint32_t above = round == 0 ? 0u : (round == 1 ? 0xffe00000u : 0xfffffc00u);
+        for (int i = tid; i < BINS; i += ST) hist[i] = 0;
+        __syncthreads();
+        for (int i0 = s0; i0 < s1; i0 += 32 * LD) {
+            float x[LD];
+            load_part(acc, i0 + lane, s1, x);
+#pragma unroll
+            for (int j = 0; j < LD; ++j) {
+                const uint32_t u = order_bits(x[j]);
+                if (i0 + 32 * j + lane < s1 && (u & above) == prefix) atomicAdd(&hist[(u >> shift) & mask], 1);
+            }
+        }
+        cluster.sync();
+        // every CTA adds up its share of the bins over the cluster and hands the sums to all
+        const int share = BINS / cs;
+        for (int i = tid; i < share; i += ST) {
+            const int bin = cr * share + i;
+            int s = 0;
+            for (int r = 0; r < cs; ++r) s += cluster.map_shared_rank(hist, r)[bin];
+            for (int r = 0; r < cs; ++r) cluster.map_shared_rank(sums, r)[bin] = s;
+        }
+        cluster.sync();
+        // the digit in which the budget runs out, from the highest down: thread t has the bins
+        // 2047 - 2t and 2046 - 2t
+        const int c0 = sums[BINS - 1 - 2 * tid], c1 = sums[BINS - 2 - 2 * tid];
+        int total;
+        const int over = block_scan(c0 + c1, scratch, &total);
+        if (over < want && over + c0 >= want) { digit = BINS - 1 - 2 * tid; rest = want - over; }
+        else if (over + c0 < want && over + c0 + c1 >= want) { digit = BINS - 2 - 2 * tid; rest = want - over - c0; }
+        __syncthreads();
+        prefix |= static_cast<uint32_t>(digit) << shift;
+        want = rest;
+        __syncthreads();
+    }
+    // T = prefix; of the rows equal to it the first `want` are kept
+    int gt = 0, eq = 0;
+    for (int i0 = s0; i0 < s1; i0 += 32 * LD) {
+        float x[LD];
+        load_part(acc, i0 + lane, s1, x);
+#pragma unroll
+        for (int j = 0; j < LD; ++j) {
+            const bool in = i0 + 32 * j + lane < s1;
+            const uint32_t u = order_bits(x[j]);
+            gt += in && u > prefix;
+            eq += in && u == prefix;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        gt += __shfl_xor_sync(0xffffffffu, gt, o);
+        eq += __shfl_xor_sync(0xffffffffu, eq, o);
+    }
+    int gt_all, eq_all;
+    int gt_at = block_scan(lane == 0 ? gt : 0, scratch, &gt_all);
+    int eq_at = block_scan(lane == 0 ? eq : 0, scratch, &eq_all);
+    if (tid == 0) { count2[0] = gt_all; count2[1] = eq_all; }
+    cluster.sync();
+    if (tid < 2) {
+        int s = 0;
+        for (int r = 0; r < cr; ++r) s += cluster.map_shared_rank(count2, r)[tid];
+        before2[tid] = s;
+    }
+    cluster.sync();                                             // also: no CTA leaves while it is read
+    gt_at = __shfl_sync(0xffffffffu, gt_at, 0) + before2[0];
+    eq_at = __shfl_sync(0xffffffffu, eq_at, 0) + before2[1];
+    const uint32_t lt = (1u << lane) - 1u;
+    for (int i0 = s0; i0 < s1; i0 += 32 * LD) {
+        float x[LD];
+        load_part(acc, i0 + lane, s1, x);
+#pragma unroll
+        for (int j = 0; j < LD; ++j) {
+            const int i = i0 + 32 * j + lane;
+            const uint32_t u = order_bits(x[j]);
+            const uint32_t mg = __ballot_sync(0xffffffffu, i < s1 && u > prefix);
+            const uint32_t me = __ballot_sync(0xffffffffu, i < s1 && u == prefix);
+            const int g = gt_at + __popc(mg & lt), e = eq_at + __popc(me & lt);
+            if (((mg >> lane) & 1u) || (((me >> lane) & 1u) && e < want)) idx[first + g + min(e, want)] = first + i;
+            gt_at += __popc(mg);
+            eq_at += __popc(me);
+        }
+    }
+}
+
+// Rows to their new places.  ROW: bytes of a K (V) row; 16 bytes per lane, 512 / ROW rows of K
+// and V each per step of a warp, UN steps in flight.
+template <int ROW>
+__global__ void __launch_bounds__(256) evict_move_kernel(EvictArgs a, int64_t keep, int blocks) {
+    constexpr int LPR = ROW / 16;                               // lanes per row
+    constexpr int RPS = LPR > 32 ? 0 : 32 / LPR;                // rows per step
+    constexpr int UN = 4;
+    static_assert(RPS >= 1, "a row spans at most a warp");
+    const int b = blockIdx.x / blocks;
+    const int lane = threadIdx.x & 31;
+    const int64_t w = static_cast<int64_t>(blockIdx.x - b * blocks) * 8 + (threadIdx.x >> 5);
+    const int64_t r0 = w * RPS * UN;
+    const int32_t* idx = a.idx + b * keep;
+    const uint4* k = static_cast<const uint4*>(a.k) + b * a.cap * LPR;
+    const uint4* v = static_cast<const uint4*>(a.v) + b * a.cap * LPR;
+    uint4* ko = static_cast<uint4*>(a.k_out) + b * a.out_cap * LPR;
+    uint4* vo = static_cast<uint4*>(a.v_out) + b * a.out_cap * LPR;
+    const int c = lane % LPR;
+    int src[UN];
+    uint4 kx[UN], vx[UN];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+        const int64_t r = r0 + u * RPS + lane / LPR;
+        src[u] = r < keep ? __ldg(idx + r) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+        if (src[u] >= 0) {
+            kx[u] = __ldg(k + static_cast<int64_t>(src[u]) * LPR + c);
+            vx[u] = __ldg(v + static_cast<int64_t>(src[u]) * LPR + c);
+        }
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+        if (src[u] >= 0) {
+            const int64_t r = r0 + u * RPS + lane / LPR;
+            ko[r * LPR + c] = kx[u];
+            vo[r * LPR + c] = vx[u];
+            if (c == 0) {
+                const int64_t s = b * a.cap + src[u], d = b * a.out_cap + r;
+                if (a.acc_out) a.acc_out[d] = __ldg(a.acc + s);
+                if (a.kv_dtype == HS2_E4M3) {
+                    a.k_scale_out[d] = __ldg(a.k_scale + s);
+                    a.v_scale_out[d] = __ldg(a.v_scale + s);
+                }
+            }
+        }
+}
+
+template <int ROW>
+void move(const EvictArgs& a, int64_t keep, cudaStream_t st) {
+    constexpr int rows = 8 * 4 * (32 / (ROW / 16));             // per CTA
+    const int blocks = static_cast<int>((keep + rows - 1) / rows);
+    evict_move_kernel<ROW><<<static_cast<unsigned>(blocks) * a.batch, 256, 0, st>>>(a, keep, blocks);
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
+    const int64_t keep = static_cast<int64_t>(a.sinks) + a.window + a.budget;
+    // CTAs per sequence: as many as keep the batch on the SMs at once, up to the portable
+    // cluster size, and no more than leaves each a few thousand rows
+    int cs = 1;
+    while (cs < 8 && 2 * cs * a.batch <= num_sms() && a.cap > static_cast<int64_t>(cs) * 4096) cs *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * cs);
+    cfg.blockDim = dim3(ST);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cs; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+    if (e != cudaSuccess) return e;
+    const int row = a.head_dim * (a.kv_dtype == HS2_F32 ? 4 : (a.kv_dtype == HS2_BF16 ? 2 : 1));
+    if (row == 64) move<64>(a, keep, st);
+    else if (row == 128) move<128>(a, keep, st);
+    else if (row == 256) move<256>(a, keep, st);
+    else move<512>(a, keep, st);
+    return cudaGetLastError();
+}
+
+}  // namespace hs2
