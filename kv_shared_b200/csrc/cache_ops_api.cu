@@ -88,7 +88,7 @@ size_t hs2_window_workspace_size(const hs2_attn_desc* desc, int32_t sinks) {
     if (check_attn(desc) != HS2_OK || desc->window < 1 || sinks < 0) return 0;
     const WindowPlan p = plan_window(desc->batch, desc->n_q, desc->heads, desc->kv_dtype, desc->window, sinks,
                                      desc->max_ctx);
-    return kStatusBytes + window_ws_bytes(desc->batch, desc->n_q, desc->heads, desc->head_dim, p.splits);
+    return kStatusBytes + window_ws_bytes(desc->batch, desc->n_q, desc->heads, desc->head_dim, p);
 }
 
 hs2_status hs2_window_attn(const hs2_attn_desc* desc, int32_t sinks, const void* q, const void* k, const void* v,
@@ -105,7 +105,7 @@ hs2_status hs2_window_attn(const hs2_attn_desc* desc, int32_t sinks, const void*
     if (!aligned4(n_rows) || !aligned4(k_scale) || !aligned4(v_scale)) return HS2_ERR_INVALID_ARG;
     const WindowPlan plan = plan_window(desc->batch, desc->n_q, desc->heads, desc->kv_dtype, desc->window, sinks,
                                         desc->max_ctx);
-    if (ws_bytes < kStatusBytes + window_ws_bytes(desc->batch, desc->n_q, desc->heads, desc->head_dim, plan.splits))
+    if (ws_bytes < kStatusBytes + window_ws_bytes(desc->batch, desc->n_q, desc->heads, desc->head_dim, plan))
         return HS2_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     WindowArgs a{};
@@ -116,8 +116,11 @@ hs2_status hs2_window_attn(const hs2_attn_desc* desc, int32_t sinks, const void*
     a.kv_dtype = desc->kv_dtype; a.scale = eff_scale(desc); a.o = o; a.lse = lse;
     a.splits = plan.splits; a.status = reinterpret_cast<uint32_t*>(ws);
     const size_t flat = static_cast<size_t>(desc->batch) * desc->n_q * desc->heads;
+    a.tile = plan.tile;
+    a.wide = ws + kStatusBytes;
+    a.wide_rows = plan.wide_rows;
     if (plan.splits > 1) {
-        a.part_o = reinterpret_cast<float*>(ws + kStatusBytes);
+        a.part_o = reinterpret_cast<float*>(ws + kStatusBytes + window_wide_bytes(desc->batch, desc->head_dim, plan));
         a.part_ml = reinterpret_cast<float2*>(a.part_o + flat * plan.splits * desc->head_dim);
     }
     return from_cuda(launch_window(a, reinterpret_cast<cudaStream_t>(stream)));

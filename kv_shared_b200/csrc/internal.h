@@ -281,14 +281,24 @@ struct WindowArgs {
     float* part_o;           // splits > 1: [split][B * n_q * H][D] unnormalised O
     float2* part_ml;         //             [split][B * n_q * H] (max, sum) in log2 units
     int splits;
+    bool tile;               // the tcgen05 kernel for chunks
+    void* wide;              // tile on e4m3: [2][B][wide_rows][D] bf16, K and V rows widened
+    int64_t wide_rows;
     uint32_t* status;
 };
 struct WindowPlan {
+    bool tile;
     int splits;              // parts the keys of each tile are cut into
+    int64_t wide_rows;       // 0: none
 };
 WindowPlan plan_window(int batch, int n_q, int heads, int kv_dtype, int window, int sinks, int64_t max_ctx);
-size_t window_ws_bytes(int batch, int n_q, int heads, int head_dim, int splits);
+size_t window_wide_bytes(int batch, int head_dim, const WindowPlan& p);
+size_t window_ws_bytes(int batch, int n_q, int heads, int head_dim, const WindowPlan& p);
 cudaError_t launch_window(const WindowArgs& a, cudaStream_t st);
+
+int window_sink_rows(int sinks, int64_t max_ctx);
+int64_t window_wide_rows(int n_q, int window, int sinks, int64_t max_ctx);
+cudaError_t launch_window_tile(const WindowArgs& a, cudaStream_t st);
 
 // ---------------------------------------------------------------- accumulated weight
 struct AccumArgs {

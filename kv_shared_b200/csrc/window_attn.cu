@@ -29,6 +29,7 @@ constexpr int kMinSplitKeys = 512;               // keys per CTA below which a s
 constexpr int F_ROWS = 64;                       // fp32: (row, head) pairs per CTA
 constexpr int F_KEYS = 32;                       // fp32: keys per tile
 constexpr int kMinSplitKeysF32 = 256;
+constexpr int64_t kTilePairs = 129;               // (row, head) pairs per sequence from which the tcgen05 kernel is taken
 
 // Four e4m3 codes -> two bf16 pairs, exact.
 __device__ __forceinline__ void codes_to_bf16(uint32_t v, uint32_t& lo, uint32_t& hi) {
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a) {
                     p0 *= f.vs[2 * h];
                     p1 *= f.vs[2 * h + 1];
                 }
-                // P in bf16: one rounding of 2^-9 relative per weight, the MMA's operand type
+                // P in bf16: one rounding of at most 2^-8 relative per weight, the MMA's operand type
                 pa[2 * h + r] = pack_bf16(p0, p1);
             }
         if (KV8) {
@@ -460,10 +461,11 @@ __global__ void __launch_bounds__(128) window_join_kernel(WindowArgs a) {
             const float2 y = *reinterpret_cast<const float2*>(src);
             x[0] = y.x; x[1] = y.y;
         }
-        const float c = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mx);
+        const bool some = ml.x != -INFINITY;         // a part without keys may have left no O
+        const float c = some ? exp2f(ml.x - mx) : 0.f;
         sum = fmaf(c, ml.y, sum);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = fmaf(c, x[i], acc[i]);
+        for (int i = 0; i < PER; ++i) acc[i] = fmaf(c, some ? x[i] : 0.f, acc[i]);
     }
     const float inv = 1.f / sum;
     T* dst = static_cast<T*>(a.o) + flat * D + lane * PER;
@@ -503,8 +505,11 @@ cudaError_t launch_join(const WindowArgs& a, cudaStream_t st) {
 
 WindowPlan plan_window(int batch, int n_q, int heads, int kv_dtype, int window, int sinks, int64_t max_ctx) {
     const bool f32 = kv_dtype == HS2_F32;
-    const int rows = f32 ? F_ROWS : 16;
-    const int64_t tiles = (static_cast<int64_t>(n_q) * heads + rows - 1) / rows * batch;
+    const int64_t pairs = static_cast<int64_t>(n_q) * heads;
+    WindowPlan p{};
+    p.tile = !f32 && pairs >= kTilePairs;
+    const int rows = f32 ? F_ROWS : (p.tile ? 256 : 16);
+    const int64_t tiles = (pairs + rows - 1) / rows * batch;
     // keys of a tile: its rows' windows and the sinks, at most the whole context
     int64_t keys = static_cast<int64_t>(window) + rows / heads + sinks + kSinkPad;
     if (keys > max_ctx + kSinkPad) keys = max_ctx + kSinkPad;
@@ -512,20 +517,25 @@ WindowPlan plan_window(int batch, int n_q, int heads, int kv_dtype, int window, 
     int64_t s = num_sms() * (f32 ? 2 : 1) / tiles;
     const int64_t most = keys / (f32 ? kMinSplitKeysF32 : kMinSplitKeys);
     if (s > most) s = most;
-    WindowPlan p;
     p.splits = s < 1 ? 1 : static_cast<int>(s);
+    if (p.tile && kv_dtype == HS2_E4M3) p.wide_rows = window_wide_rows(n_q, window, sinks, max_ctx);
     return p;
 }
 
-size_t window_ws_bytes(int batch, int n_q, int heads, int head_dim, int splits) {
-    if (splits <= 1) return 0;
-    return static_cast<size_t>(batch) * n_q * heads * splits * (head_dim * sizeof(float) + sizeof(float2));
+size_t window_wide_bytes(int batch, int head_dim, const WindowPlan& p) {
+    return static_cast<size_t>(2) * batch * p.wide_rows * head_dim * 2;
+}
+
+size_t window_ws_bytes(int batch, int n_q, int heads, int head_dim, const WindowPlan& p) {
+    const size_t parts = p.splits <= 1 ? 0 : static_cast<size_t>(batch) * n_q * heads * p.splits * (head_dim * sizeof(float) + sizeof(float2));
+    return window_wide_bytes(batch, head_dim, p) + parts;
 }
 
 cudaError_t launch_window(const WindowArgs& a, cudaStream_t st) {
     cudaError_t e;
     const bool d128 = a.head_dim == 128;
-    if (a.kv_dtype == HS2_F32) e = d128 ? launch_f32<128>(a, st) : launch_f32<64>(a, st);
+    if (a.tile) e = launch_window_tile(a, st);
+    else if (a.kv_dtype == HS2_F32) e = d128 ? launch_f32<128>(a, st) : launch_f32<64>(a, st);
     else if (a.kv_dtype == HS2_BF16) e = d128 ? launch_rows<128, false>(a, st) : launch_rows<64, false>(a, st);
     else e = d128 ? launch_rows<128, true>(a, st) : launch_rows<64, true>(a, st);
     if (e != cudaSuccess || a.splits == 1) return e;

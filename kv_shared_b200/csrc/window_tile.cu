@@ -1,0 +1,624 @@
+// window_tile.cu -- attention over a sliding window and the first tokens (sinks) for chunks
+// of query rows, on tcgen05.
+//
+// The query at position p attends to rows j <= p with j > p - W or j < S.  All heads share
+// the one K/V head, so 256 consecutive (row, head) pairs of a sequence are stacked in the
+// MMA's M dimension as two halves of 128, and both halves consume every K and V tile that
+// the CTA loads.  The keys that any of the 256 pairs sees form one list (KeyList); it is cut
+// into tiles of 128, the last one as short as the list allows (a multiple of 16), so that a
+// window of 128 costs 160 columns and not 256.
+//
+// Per half and tile:  S = Q K^T into tensor memory; one thread per pair reads its row of S,
+// masks it, and forms P = 2^(S sc2 - m), which goes back over S as packed bf16 and is the A
+// operand of O += P V.  m is a reference that trails the running maximum by at most 2^8: it
+// moves, and O is rescaled in place, only when the maximum rises by more than 8 in log2
+// units, which after a row's first tile is rare; sums and O are fp32 and P keeps bf16's
+// relative rounding of 2^-8 whatever its magnitude, so nothing is lost by it.
+//
+// S(i + 1) of a half is issued right behind PV(i) of the same half by the same thread: the
+// tensor pipe executes one thread's MMAs in issue order, so P(i) has been read before S(i + 1)
+// overwrites it, and S(i + 1) being complete means that O holds PV(i).  While one half's
+// threads form P the tensor cores work for the other half.
+//
+// Work items (sequence, 256 pairs, part of the keys) are dealt to one persistent CTA per SM,
+// and the roles run ahead of one another across items: the next item's Q, K and V are loaded
+// and its S formed while the epilogue of this one still reads O.
+//
+// Roles (512 threads): warps 0-3 and 4-7 the softmax of halves 0 and 1, warps 8-11 the
+// epilogue, warp 12 the loads, one thread of warp 13 the MMAs.  The softmax threads hold a row
+// of S in registers (192 registers each, taken from the other roles).  Every wait is bounded;
+// a wait that gives up flags the status word and makes all roles leave their loops.
+//
+// e4m3 caches: the codes of the rows that the call attends to are first widened to bf16
+// (exact) in the workspace; the rows' scales multiply S and P in fp32.
+#include "common.cuh"
+#include "f32x2.cuh"
+#include "internal.h"
+#include "tcgen05.cuh"
+#include "window_keys.cuh"
+
+namespace hs2 {
+namespace {
+
+constexpr int KT = 128;                         // keys per tile
+constexpr int MH = 128;                         // pairs per half
+constexpr int NT = 512;
+constexpr int STAGES = 4;                       // K and V tiles in flight, K(t) at 2t, V(t) at 2t + 1
+constexpr int SC_SLOTS = 4;                     // tiles whose scales are held (at most 3 are live)
+constexpr float kLag = 8.f;                     // log2 units the reference may trail the maximum by
+constexpr uint32_t kPolyGroups = 0x11;          // of 8 groups of 4 columns: which take the FMA pipe
+
+template <int D>
+struct Shape {
+    static constexpr int ROW = D * 2;                          // bytes of a bf16 row
+    static constexpr int BOXES = D / 64;                       // 64-column swizzled boxes per tile
+    static constexpr int BOX = KT * 128;                       // bytes of a box
+    static constexpr int TILE = BOXES * BOX;
+    static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + SC_SLOTS * 2 * KT * 4;
+};
+
+struct TileArgs {
+    WindowArgs w;
+    int64_t items;                              // batch * tiles * splits
+    int tiles;                                  // 256-pair tiles per sequence
+    int64_t cap;                                // rows per sequence of the maps' K and V
+    int s16;                                    // e4m3: widened sink rows per sequence
+    uint32_t* status;
+};
+
+// First widened cache row of a sequence: its first row's window start, or 0 where the sinks
+// reach it (then no sink lies before the window's range of any row).
+__device__ __forceinline__ int widened_lo(int base, int window, int sinks) {
+    const int lo = max(0, base - window + 1);
+    return sinks >= lo ? 0 : lo;
+}
+
+// One work item: which pairs and which tiles of their key list.
+struct Work {
+    int b, f0, f_last, base, t0, t1, split, shift;             // shift: map row of cache row r in the window part
+    KeyList kl;
+    __device__ __forceinline__ Work() : kl(0, 0, 1, 0) {}
+    // false: no pairs in use.  t0 == t1: no keys in this part.
+    __device__ __forceinline__ bool get(const TileArgs& a, int64_t item) {
+        const WindowArgs& w = a.w;
+        split = static_cast<int>(item % w.splits);
+        const int64_t rest = item / w.splits;
+        b = static_cast<int>(rest / a.tiles);
+        f0 = static_cast<int>(rest - static_cast<int64_t>(b) * a.tiles) * 2 * MH;
+        const int live = live_rows(w.n_rows, b, w.n_q);
+        if (f0 >= live * w.heads) return false;
+        base = checked_base(w.q_pos0, b, live, w.max_ctx, a.status);
+        f_last = min(f0 + 2 * MH - 1, live * w.heads - 1);
+        kl = KeyList(base + f0 / w.heads, base + f_last / w.heads, w.window, w.sinks);
+        const int n = (kl.total + KT - 1) / KT, per = (n + w.splits - 1) / w.splits;
+        t0 = min(n, split * per);
+        t1 = min(n, t0 + per);
+        shift = w.kv_dtype == HS2_E4M3 ? a.s16 - widened_lo(base, w.window, w.sinks) : 0;
+        return true;
+    }
+    __device__ __forceinline__ int halves() const { return f_last - f0 >= MH ? 2 : 1; }
+    // columns of tile t, to a multiple of 16
+    __device__ __forceinline__ int cols(int t) const { return min(KT, (kl.total - t * KT + 15) & ~15); }
+};
+
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
+    if (*abort_flag) return false;
+    if (!mbar_wait(bar, parity, status)) { *abort_flag = 1; return false; }
+    return true;
+}
+__device__ __forceinline__ bool spin_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
+    if (*abort_flag) return false;
+    if (!mbar_wait_spin(bar, parity, status)) { *abort_flag = 1; return false; }
+    return true;
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    umma::fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+template <int R>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+// K-major descriptor of the 16-wide K step kk, MN-major descriptor of the 16-row K step kk
+__device__ __forceinline__ uint64_t kmajor(uint32_t base, int kk) {
+    return umma::sdesc_sw128(base + (kk >> 2) * (KT * 128) + (kk & 3) * 32, 16, 1024);
+}
+__device__ __forceinline__ uint64_t mnmajor(uint32_t base, int kk) {
+    return umma::sdesc_sw128(base + kk * 2048, KT * 128, 1024);
+}
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
+template <int D, bool KV8>
+__global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constant__ CUtensorMap qmap,
+                                                           const __grid_constant__ CUtensorMap kmap,
+                                                           const __grid_constant__ CUtensorMap vmap,
+                                                           const __grid_constant__ CUtensorMap kmap16,
+                                                           const __grid_constant__ CUtensorMap vmap16,
+                                                           const __grid_constant__ TileArgs a) {
+    using Sh = Shape<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* qs = smem;                                        // Q of halves 0, 1
+    uint8_t* st = smem + 2 * Sh::TILE;                         // K and V stages
+    float* ring = reinterpret_cast<float*>(st + STAGES * Sh::TILE);       // [SC_SLOTS][2][KT] scales (e4m3)
+    __shared__ uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], s_full[2], p_full[2], o_full[2],
+        o_empty[2], st_full[2][2], sc_full[SC_SLOTS];
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile int abort_flag;
+    // (m, l) by item parity and half: the softmax may finish an item while the epilogue still has
+    // the one before (the next one's S waits for it), hence two of these and of their barriers
+    __shared__ float2 stat[2][2][MH];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(&q_full[h], 1); mbar_init(&q_empty[h], 1); mbar_init(&s_full[h], 1); mbar_init(&p_full[h], 4);
+            mbar_init(&o_full[h], 1); mbar_init(&o_empty[h], 4);
+            mbar_init(&st_full[0][h], 4); mbar_init(&st_full[1][h], 4);
+        }
+        for (int s = 0; s < STAGES; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
+        for (int s = 0; s < SC_SLOTS; ++s) mbar_init(&sc_full[s], 32);
+        fence_mbar_init();
+        abort_flag = 0;
+    }
+    if (warp == 13) umma::tmem_alloc(&tmem_base, 512);
+    umma::fence_before();
+    __syncthreads();
+    umma::fence_after();
+    const uint32_t tmem = tmem_base;            // S/P of half h at column 128 h, O of half h at 256 + 128 h
+
+    if (warp < 8) {
+        // ---------------------------------------------------------------- softmax
+        regs_inc<192>();
+        const int h = warp >> 2, quarter = warp & 3, m_row = quarter * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t ts = tmem + lanes + 128 * h, to = tmem + lanes + 256 + 128 * h;
+        const float sc2 = a.w.scale * kLog2e;
+        uint32_t gt = 0, ht = 0, hi = 0;        // tiles so far; tiles and items of this half
+        bool ok = true;
+        for (int64_t item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
+            Work w;
+            if (!w.get(a, item) || w.t0 == w.t1) continue;
+            if (h >= w.halves()) { gt += w.t1 - w.t0; continue; }
+            // this pair sees list entries [lo_u, hi_u] and those below s_u
+            const int f = w.f0 + MH * h + m_row;
+            int lo_u = 0, hi_u = -1, s_u = 0;
+            if (f <= w.f_last) {
+                const int p = w.base + f / a.w.heads;
+                lo_u = max(p - a.w.window + 1 - w.kl.lo, 0) + w.kl.s_pad;
+                hi_u = p - w.kl.lo + w.kl.s_pad;
+                s_u = w.kl.lo > 0 ? w.kl.s_eff : min(a.w.sinks, p + 1);
+            }
+            float m = -INFINITY, l = 0.f;
+            for (int t = w.t0; t < w.t1; ++t, ++gt, ++ht) {
+                if (!__all_sync(0xffffffffu, wait_or_abort(&s_full[h], ht & 1, &abort_flag, a.status))) { ok = false; break; }
+                umma::fence_after();
+                const int u0 = t * KT, nc = (w.cols(t) + 31) >> 5;
+                // V rows of entries that hold no key may hold anything, and 0 * NaN would poison O
+                if (!KV8 && (u0 + KT > w.kl.total || (u0 < w.kl.s_pad && w.kl.s_eff < w.kl.s_pad))) {
+                    const int r = quarter * 32 + lane;
+                    const uint32_t vi = 2 * gt + 1;
+                    if (r < w.cols(t) && w.kl.row(u0 + r) < 0 &&
+                        wait_or_abort(&kv_full[vi % STAGES], (vi / STAGES) & 1, &abort_flag, a.status)) {
+                        uint8_t* vrow = st + (vi % STAGES) * Sh::TILE + r * 128;
+#pragma unroll
+                        for (int c = 0; c < Sh::BOXES * 8; ++c)
+                            *reinterpret_cast<uint4*>(vrow + (c >> 3) * Sh::BOX + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        umma::fence_proxy_async();
+                    }
+                    __syncwarp();
+                }
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c < nc) umma::tmem_ld32(ts + 32 * c, s[c]);
+                if (KV8 && !__all_sync(0xffffffffu, wait_or_abort(&sc_full[gt % SC_SLOTS], (gt / SC_SLOTS) & 1, &abort_flag,
+                                                                  a.status))) { ok = false; break; }
+                umma::tmem_ld_wait();
+                const float* ksc = ring + (gt % SC_SLOTS) * 2 * KT;
+                const bool masked = __any_sync(0xffffffffu, u0 < lo_u || u0 + KT - 1 > hi_u);
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c < nc) {
+                        if (KV8) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4) {
+                                const float4 k4 = *reinterpret_cast<const float4*>(ksc + 32 * c + j);
+                                s[c][j] = __float_as_uint(__uint_as_float(s[c][j]) * k4.x);
+                                s[c][j + 1] = __float_as_uint(__uint_as_float(s[c][j + 1]) * k4.y);
+                                s[c][j + 2] = __float_as_uint(__uint_as_float(s[c][j + 2]) * k4.z);
+                                s[c][j + 3] = __float_as_uint(__uint_as_float(s[c][j + 3]) * k4.w);
+                            }
+                        }
+                        if (masked) {
+                            const int cb = u0 + 32 * c;
+                            const uint32_t see = (bits_below(hi_u - cb + 1) & ~bits_below(lo_u - cb)) | bits_below(s_u - cb);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (!((see >> j) & 1u)) s[c][j] = 0xff800000u;              // -inf
+                        }
+                        float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            m0 = max3(m0, __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
+                            m1 = max3(m1, __uint_as_float(s[c][j + 2]), __uint_as_float(s[c][j + 3]));
+                        }
+                        mx = max3(mx, m0, m1);
+                    }
+                mx *= sc2;
+                if (mx > m) {
+                    if (m == -INFINITY) m = mx;              // nothing summed yet: l and O's row are zero
+                }
+                const bool move = mx > m + kLag;
+                if (__any_sync(0xffffffffu, move)) {
+                    const float c = move ? ex2(m - mx) : 1.f;
+                    l *= c;
+                    if (move) m = mx;
+                    if (t > w.t0) {
+#pragma unroll 1
+                        for (int d = 0; d < D; d += 16) {
+                            uint32_t o[16];
+                            umma::tmem_ld32x16(to + d, o);
+                            umma::tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * c);
+                            umma::tmem_st32x16(to + d, o);
+                        }
+                        umma::tmem_st_wait();
+                    }
+                }
+                const float off = m == -INFINITY ? 0.f : m;
+                const float2 s2 = make_float2(sc2, sc2), nm = make_float2(-off, -off);
+                float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c < nc) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float2 x0 = fma2(make_float2(__uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1])), s2, nm);
+                            const float2 x1 = fma2(make_float2(__uint_as_float(s[c][j + 2]), __uint_as_float(s[c][j + 3])), s2, nm);
+                            float2 p0, p1;
+                            if ((kPolyGroups >> (j / 4)) & 1u) {
+                                p0 = exp2_poly2(x0);
+                                p1 = exp2_poly2(x1);
+                            } else {
+                                p0 = make_float2(ex2(x0.x), ex2(x0.y));
+                                p1 = make_float2(ex2(x1.x), ex2(x1.y));
+                            }
+                            sum0 = add2(sum0, p0);
+                            sum1 = add2(sum1, p1);
+                            if (KV8) {
+                                const float4 v4 = *reinterpret_cast<const float4*>(ksc + KT + 32 * c + j);
+                                p0.x *= v4.x; p0.y *= v4.y; p1.x *= v4.z; p1.y *= v4.w;
+                            }
+                            pk[j / 2] = pack_bf16(p0.x, p0.y);
+                            pk[j / 2 + 1] = pack_bf16(p1.x, p1.y);
+                        }
+                        umma::tmem_st32x16(ts + 16 * c, pk);
+                    }
+                l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+                umma::tmem_st_wait();
+                warp_arrive(&p_full[h]);
+            }
+            if (!ok) break;
+            stat[hi & 1][h][m_row] = make_float2(m, l);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&st_full[hi & 1][h]);
+            ++hi;
+        }
+    } else if (warp < 12) {
+        // ---------------------------------------------------------------- epilogue
+        regs_dec<72>();
+        const int quarter = warp & 3, m_row = quarter * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        uint32_t hi[2] = {0, 0};
+        bool ok = true;
+        const int64_t all = static_cast<int64_t>(a.w.batch) * a.w.n_q * a.w.heads;
+        for (int64_t item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
+            Work w;
+            if (!w.get(a, item)) continue;
+            const int nh = w.halves();
+            for (int h = 0; h < nh; ++h) {
+                const int f = w.f0 + MH * h + m_row;
+                const int64_t flat = static_cast<int64_t>(w.b) * a.w.n_q * a.w.heads + f;
+                const int64_t at = static_cast<int64_t>(w.split) * all + flat;
+                const bool mine = f <= w.f_last;
+                if (w.t0 == w.t1) {                              // only of split keys: an empty part
+                    if (mine) a.w.part_ml[at] = make_float2(-INFINITY, 0.f);
+                    continue;
+                }
+                if (!__all_sync(0xffffffffu, wait_or_abort(&st_full[hi[h] & 1][h], (hi[h] >> 1) & 1, &abort_flag, a.status) &&
+                                                 wait_or_abort(&o_full[h], hi[h] & 1, &abort_flag, a.status))) { ok = false; break; }
+                umma::fence_after();
+                const float2 ml = stat[hi[h] & 1][h][m_row];
+                const float inv = a.w.splits == 1 ? 1.f / ml.y : 1.f;
+#pragma unroll
+                for (int d = 0; d < D; d += 32) {
+                    uint32_t o[32];
+                    umma::tmem_ld32(tmem + lanes + 256 + 128 * h + d, o);
+                    umma::tmem_ld_wait();
+                    if (d + 32 == D) warp_arrive(&o_empty[h]);
+                    if (mine) {
+                        if (a.w.splits == 1) {
+                            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.w.o) + flat * D + d);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                dst[j] = make_uint4(
+                                    pack_bf16(__uint_as_float(o[8 * j]) * inv, __uint_as_float(o[8 * j + 1]) * inv),
+                                    pack_bf16(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv),
+                                    pack_bf16(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv),
+                                    pack_bf16(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv));
+                        } else {
+                            uint4* dst = reinterpret_cast<uint4*>(a.w.part_o + at * D + d);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        }
+                    }
+                }
+                if (mine) {
+                    if (a.w.splits > 1) a.w.part_ml[at] = ml;
+                    else if (a.w.lse) a.w.lse[flat] = (ml.x + log2f(ml.y)) * kLn2;
+                }
+                ++hi[h];
+            }
+        }
+    } else {
+        regs_dec<56>();
+        if (warp == 12 && (KV8 || lane == 0)) {
+            // ------------------------------------------------------------ loads
+            uint32_t n = 0, gt = 0, hi[2] = {0, 0};               // stage uses, tiles, items per half
+            bool ok = true;
+            for (int64_t item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
+                Work w;
+                if (!w.get(a, item) || w.t0 == w.t1) continue;
+                const int nh = w.halves();
+                const int krow = static_cast<int>(w.b * a.cap);
+                for (int t = w.t0; ok && t < w.t1; ++t, ++gt) {
+                    const int u0 = t * KT, groups = w.cols(t) >> 4;
+                    for (int kv = 0; kv < 2; ++kv, ++n) {
+                        const int s = n % STAGES;
+                        if (lane == 0 && n >= STAGES)
+                            ok = wait_or_abort(&kv_empty[s], ((n / STAGES) - 1) & 1, &abort_flag, a.status);
+                        if (KV8) ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            uint8_t* dst = st + s * Sh::TILE;
+                            if (u0 >= w.kl.s_pad && groups > 4) {                // one box of 128 rows
+                                const CUtensorMap* map = kv ? &vmap : &kmap;
+                                const int row = krow + w.kl.lo + w.shift + u0 - w.kl.s_pad;
+                                mbar_arrive_expect_tx(&kv_full[s], Sh::TILE);
+                                for (int c = 0; c < Sh::BOXES; ++c)
+                                    tma_load_2d(dst + c * Sh::BOX, map, &kv_full[s], 64 * c, row);
+                            } else {                                             // boxes of 16 rows
+                                const CUtensorMap* map = kv ? &vmap16 : &kmap16;
+                                mbar_arrive_expect_tx(&kv_full[s], groups * 16 * Sh::ROW);
+                                for (int g = 0; g < groups; ++g) {
+                                    const int u = u0 + 16 * g;
+                                    const int row = krow + (u < w.kl.s_pad ? u : w.kl.lo + w.shift + u - w.kl.s_pad);
+                                    for (int c = 0; c < Sh::BOXES; ++c)
+                                        tma_load_2d(dst + c * Sh::BOX + g * 2048, map, &kv_full[s], 64 * c, row);
+                                }
+                            }
+                        }
+                        if (kv == 0) {
+                            if (KV8) {          // the tile's 128 K and V scales, each lane's copies arriving as they land
+                                float* slot = ring + (gt % SC_SLOTS) * 2 * KT;
+                                const int64_t seq0 = static_cast<int64_t>(w.b) * a.w.cap;
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const int key = w.kl.row(u0 + lane + 32 * j);
+                                    const int64_t src = seq0 + max(key, 0);
+                                    cp_async4_zfill(slot + lane + 32 * j, a.w.k_scale + src, key >= 0);
+                                    cp_async4_zfill(slot + KT + lane + 32 * j, a.w.v_scale + src, key >= 0);
+                                }
+                                cp_async_arrive_noinc(&sc_full[gt % SC_SLOTS]);
+                            }
+                            if (t == w.t0) {
+                                for (int h = 0; ok && h < nh; ++h) {
+                                    if (lane == 0) {
+                                        if (hi[h] > 0) ok = wait_or_abort(&q_empty[h], (hi[h] - 1) & 1, &abort_flag, a.status);
+                                        if (ok) {
+                                            const int row = w.b * a.w.n_q * a.w.heads + w.f0 + MH * h;
+                                            mbar_arrive_expect_tx(&q_full[h], Sh::TILE);
+                                            for (int c = 0; c < Sh::BOXES; ++c)
+                                                tma_load_2d(qs + h * Sh::TILE + c * Sh::BOX, &qmap, &q_full[h], 64 * c, row);
+                                        }
+                                    }
+                                    if (KV8) ok = __shfl_sync(0xffffffffu, ok, 0);
+                                    ++hi[h];
+                                }
+                                if (!ok) break;
+                            }
+                        }
+                    }
+                }
+            }
+            if (KV8) asm volatile("cp.async.wait_all;" ::: "memory");
+        } else if (warp == 13 && lane == 0) {
+            // ------------------------------------------------------------ MMAs
+            constexpr uint32_t idesc_o = umma::idesc_bf16(128, D, false, true);
+            const uint32_t qb = smem_u32(qs), sb = smem_u32(st);
+            // two walks over the same tiles: S runs one tile ahead of PV
+            Work ws, wp;
+            int64_t is = blockIdx.x, ip = blockIdx.x;
+            int ts = 0, tp = 0;
+            bool have_s, have_p;
+            auto seek = [&](Work& w, int64_t& item, int& t) {
+                for (; item < a.items; item += gridDim.x)
+                    if (w.get(a, item) && w.t0 < w.t1) { t = w.t0; return true; }
+                return false;
+            };
+            have_s = seek(ws, is, ts);
+            have_p = seek(wp, ip, tp);
+            uint32_t gs = 0, gp = 0;                              // tiles of the two walks
+            uint32_t qi[2] = {0, 0}, oi[2] = {0, 0}, pi[2] = {0, 0};
+            bool ok = true, k_ready = false;
+            auto issue_s = [&](int h) {                           // S(ts) of half h
+                if (!have_s || h >= ws.halves()) return;
+                const uint32_t n = 2 * gs;
+                if (!k_ready) {
+                    if (!(ok = spin_or_abort(&kv_full[n % STAGES], (n / STAGES) & 1, &abort_flag, a.status))) return;
+                    k_ready = true;
+                }
+                if (ts == ws.t0 && !(ok = spin_or_abort(&q_full[h], qi[h] & 1, &abort_flag, a.status))) return;
+                umma::fence_after();
+                const uint32_t idesc_s = umma::idesc_bf16(128, ws.cols(ts), false, false);
+                const uint32_t kb = sb + (n % STAGES) * Sh::TILE;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    umma::mma_bf16_ss(tmem + 128 * h, kmajor(qb + h * Sh::TILE, kk), kmajor(kb, kk), idesc_s, kk > 0);
+                umma::commit(&s_full[h]);
+                if (ts + 1 == ws.t1) { umma::commit(&q_empty[h]); ++qi[h]; }
+                if (h == ws.halves() - 1) umma::commit(&kv_empty[n % STAGES]);
+            };
+            auto next_s = [&]() {
+                if (!have_s) return;
+                ++gs;
+                k_ready = false;
+                if (++ts == ws.t1) { is += gridDim.x; have_s = seek(ws, is, ts); }
+            };
+            for (int h = 0; ok && h < 2; ++h) issue_s(h);
+            next_s();
+            while (ok && have_p) {
+                const uint32_t n = 2 * gp + 1;
+                const int steps = wp.cols(tp) >> 4;
+                const bool first = tp == wp.t0, last = tp + 1 == wp.t1;
+                bool v_ready = false;
+                for (int h = 0; ok && h < 2; ++h) {
+                    if (h < wp.halves()) {
+                        if (!(ok = spin_or_abort(&p_full[h], pi[h] & 1, &abort_flag, a.status))) break;
+                        ++pi[h];
+                        if (!v_ready && !(ok = spin_or_abort(&kv_full[n % STAGES], (n / STAGES) & 1, &abort_flag, a.status))) break;
+                        v_ready = true;
+                        if (first && oi[h] > 0 && !(ok = spin_or_abort(&o_empty[h], (oi[h] - 1) & 1, &abort_flag, a.status))) break;
+                        umma::fence_after();
+                        const uint32_t vb = sb + (n % STAGES) * Sh::TILE;
+                        for (int kk = 0; kk < steps; ++kk)
+                            umma::mma_bf16_ts(tmem + 256 + 128 * h, tmem + 128 * h + 8 * kk, mnmajor(vb, kk), idesc_o,
+                                              (!first || kk > 0) ? 1u : 0u);
+                        if (last) { umma::commit(&o_full[h]); ++oi[h]; }
+                        if (h == wp.halves() - 1) umma::commit(&kv_empty[n % STAGES]);
+                    }
+                    issue_s(h);
+                }
+                next_s();
+                ++gp;
+                if (++tp == wp.t1) { ip += gridDim.x; have_p = seek(wp, ip, tp); }
+            }
+        }
+    }
+    __syncwarp();
+    umma::fence_before();
+    __syncthreads();
+    if (warp == 13) {
+        umma::fence_after();
+        umma::tmem_dealloc(tmem, 512);
+    }
+}
+
+// The rows that the call attends to, codes widened to bf16 (exact), per sequence: the sinks at
+// rows 0 .. s16 - 1, then the cache rows from the first window's start to the last position,
+// and 16 zero rows (the end of a list is read to a multiple of 16).  8 codes of K and V per
+// thread and step.
+template <int D>
+__global__ void __launch_bounds__(256) window_widen_kernel(WindowArgs a, int s16, int64_t rows,
+                                                           __nv_bfloat16* __restrict__ kw, __nv_bfloat16* __restrict__ vw) {
+    constexpr int PER = D / 8;
+    const int b = blockIdx.y;
+    const int live = live_rows(a.n_rows, b, a.n_q);
+    if (live == 0) return;
+    const int base = checked_base(a.q_pos0, b, live, a.max_ctx, a.status);
+    const int lo = widened_lo(base, a.window, a.sinks), last = base + live - 1;
+    const int64_t used = min(rows, static_cast<int64_t>(s16) + last - lo + 1 + 16);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < used * PER; i += step) {
+        const int64_t r = i / PER;
+        const int c = static_cast<int>(i - r * PER);
+        int key = -1;
+        if (r < s16) {
+            if (r < a.sinks && r <= last) key = static_cast<int>(r);
+        } else if (r - s16 <= last - lo) {
+            key = lo + static_cast<int>(r - s16);
+        }
+        uint4 ko = make_uint4(0, 0, 0, 0), vo = ko;
+        if (key >= 0) {
+            const int64_t src = (static_cast<int64_t>(b) * a.cap + key) * D + c * 8;
+            const uint2 kc = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.k) + src));
+            const uint2 vc = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.v) + src));
+            ko = make_uint4(e4m3x2_to_bf16x2(kc.x & 0xffff), e4m3x2_to_bf16x2(kc.x >> 16),
+                            e4m3x2_to_bf16x2(kc.y & 0xffff), e4m3x2_to_bf16x2(kc.y >> 16));
+            vo = make_uint4(e4m3x2_to_bf16x2(vc.x & 0xffff), e4m3x2_to_bf16x2(vc.x >> 16),
+                            e4m3x2_to_bf16x2(vc.y & 0xffff), e4m3x2_to_bf16x2(vc.y >> 16));
+        }
+        const int64_t dst = static_cast<int64_t>(b) * rows + r;
+        reinterpret_cast<uint4*>(kw + dst * D)[c] = ko;
+        reinterpret_cast<uint4*>(vw + dst * D)[c] = vo;
+    }
+}
+
+template <int D, bool KV8>
+cudaError_t launch(const WindowArgs& w, cudaStream_t st) {
+    using Sh = Shape<D>;
+    TileArgs a{};
+    a.w = w;
+    a.status = w.status;
+    a.tiles = static_cast<int>((static_cast<int64_t>(w.n_q) * w.heads + 2 * MH - 1) / (2 * MH));
+    a.items = static_cast<int64_t>(w.batch) * a.tiles * w.splits;
+    a.cap = w.cap;
+    const void* k = w.k;
+    const void* v = w.v;
+    if (KV8) {
+        a.s16 = window_sink_rows(w.sinks, w.max_ctx);
+        a.cap = w.wide_rows;
+        __nv_bfloat16* kw = static_cast<__nv_bfloat16*>(w.wide);
+        __nv_bfloat16* vw = kw + static_cast<size_t>(w.batch) * w.wide_rows * D;
+        const int64_t work = (w.wide_rows * (D / 8) + 255) / 256;
+        const int64_t most = 8 * static_cast<int64_t>(num_sms()) / w.batch + 1;
+        window_widen_kernel<D><<<dim3(static_cast<unsigned>(work < most ? work : most), w.batch), 256, 0, st>>>(
+            w, a.s16, w.wide_rows, kw, vw);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        k = kw;
+        v = vw;
+    }
+    const uint64_t pairs = static_cast<uint64_t>(w.batch) * w.n_q * w.heads, rows = static_cast<uint64_t>(w.batch) * a.cap;
+    const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    CUtensorMap qm, km, vm, km16, vm16;
+    if (!make_tmap_2d(&qm, w.q, bf, 2, D, pairs, Sh::ROW, 64, MH, true) ||
+        !make_tmap_2d(&km, k, bf, 2, D, rows, Sh::ROW, 64, KT, true) ||
+        !make_tmap_2d(&vm, v, bf, 2, D, rows, Sh::ROW, 64, KT, true) ||
+        !make_tmap_2d(&km16, k, bf, 2, D, rows, Sh::ROW, 64, 16, true) ||
+        !make_tmap_2d(&vm16, v, bf, 2, D, rows, Sh::ROW, 64, 16, true))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(window_tile_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = a.items < num_sms() ? a.items : num_sms();
+    window_tile_kernel<D, KV8><<<static_cast<unsigned>(grid), NT, Sh::SMEM, st>>>(qm, km, vm, km16, vm16, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int window_sink_rows(int sinks, int64_t max_ctx) {
+    const int64_t s = sinks < max_ctx ? sinks : max_ctx;
+    return static_cast<int>((s + kSinkPad - 1) / kSinkPad * kSinkPad);
+}
+
+int64_t window_wide_rows(int n_q, int window, int sinks, int64_t max_ctx) {
+    int64_t span = static_cast<int64_t>(window) + n_q + sinks;
+    if (span > max_ctx) span = max_ctx;
+    return window_sink_rows(sinks, max_ctx) + span + 16;
+}
+
+cudaError_t launch_window_tile(const WindowArgs& a, cudaStream_t st) {
+    if (a.kv_dtype == HS2_E4M3) return a.head_dim == 128 ? launch<128, true>(a, st) : launch<64, true>(a, st);
+    return a.head_dim == 128 ? launch<128, false>(a, st) : launch<64, false>(a, st);
+}
+
+}  // namespace hs2
