@@ -59,7 +59,7 @@ struct Shape {
 
 struct TileArgs {
     WindowArgs w;
-    int64_t items;                              // batch * tiles * splits
+    int items;                                  // batch * tiles * splits
     int tiles;                                  // 256-pair tiles per sequence
     int64_t cap;                                // rows per sequence of the maps' K and V
     int s16;                                    // e4m3: widened sink rows per sequence
@@ -73,24 +73,28 @@ __device__ __forceinline__ int widened_lo(int base, int window, int sinks) {
     return sinks >= lo ? 0 : lo;
 }
 
-// One work item: which pairs and which tiles of their key list.
+// One work item: which pairs and which tiles of their key list.  Consecutive items of a CTA
+// mostly belong to one sequence, whose position and length are kept from item to item.
 struct Work {
-    int b, f0, f_last, base, t0, t1, split, shift;             // shift: map row of cache row r in the window part
+    int b, f0, f_last, base, live, t0, t1, split, shift;       // shift: map row of cache row r in the window part
     KeyList kl;
-    __device__ __forceinline__ Work() : kl(0, 0, 1, 0) {}
+    __device__ __forceinline__ Work() : b(-1), kl(0, 0, 1, 0) {}
     // false: no pairs in use.  t0 == t1: no keys in this part.
-    __device__ __forceinline__ bool get(const TileArgs& a, int64_t item) {
+    __device__ __forceinline__ bool get(const TileArgs& a, int item) {
         const WindowArgs& w = a.w;
-        split = static_cast<int>(item % w.splits);
-        const int64_t rest = item / w.splits;
-        b = static_cast<int>(rest / a.tiles);
-        f0 = static_cast<int>(rest - static_cast<int64_t>(b) * a.tiles) * 2 * MH;
-        const int live = live_rows(w.n_rows, b, w.n_q);
+        const int rest = w.splits == 1 ? item : item / w.splits;
+        split = item - rest * w.splits;
+        const int seq = rest / a.tiles;
+        f0 = (rest - seq * a.tiles) * 2 * MH;
+        if (seq != b) {
+            b = seq;
+            live = live_rows(w.n_rows, b, w.n_q);
+            base = checked_base(w.q_pos0, b, live, w.max_ctx, a.status);
+        }
         if (f0 >= live * w.heads) return false;
-        base = checked_base(w.q_pos0, b, live, w.max_ctx, a.status);
         f_last = min(f0 + 2 * MH - 1, live * w.heads - 1);
         kl = KeyList(base + f0 / w.heads, base + f_last / w.heads, w.window, w.sinks);
-        const int n = (kl.total + KT - 1) / KT, per = (n + w.splits - 1) / w.splits;
+        const int n = (kl.total + KT - 1) / KT, per = w.splits == 1 ? n : (n + w.splits - 1) / w.splits;
         t0 = min(n, split * per);
         t1 = min(n, t0 + per);
         shift = w.kv_dtype == HS2_E4M3 ? a.s16 - widened_lo(base, w.window, w.sinks) : 0;
@@ -106,28 +110,39 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
     if (!mbar_wait(bar, parity, status)) { *abort_flag = 1; return false; }
     return true;
 }
+// the MMA warp's waits, which sit on the critical path of every handoff (whole warp)
 __device__ __forceinline__ bool spin_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
-    if (*abort_flag) return false;
-    if (!mbar_wait_spin(bar, parity, status)) { *abort_flag = 1; return false; }
-    return true;
+    bool ok = mbar_test_wait(bar, parity);                     // the common case: without a look at flag or clock
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if (!ok) ok = !*abort_flag && mbar_wait_spin(bar, parity, status);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    *abort_flag = 1;
+    return false;
 }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     umma::fence_before();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
+// One lane of a converged warp, the same every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 template <int R>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
-// K-major descriptor of the 16-wide K step kk, MN-major descriptor of the 16-row K step kk
-__device__ __forceinline__ uint64_t kmajor(uint32_t base, int kk) {
-    return umma::sdesc_sw128(base + (kk >> 2) * (KT * 128) + (kk & 3) * 32, 16, 1024);
-}
-__device__ __forceinline__ uint64_t mnmajor(uint32_t base, int kk) {
-    return umma::sdesc_sw128(base + kk * 2048, KT * 128, 1024);
-}
+// Descriptors of a tile's first K step (K-major with its two 64-column boxes, MN-major), of
+// which the steps differ in the address field alone: step kk at
+//   K-major  + (kk / 4) boxes + (kk % 4) 32 bytes,     MN-major  + kk 2048 bytes.
+__device__ __forceinline__ uint64_t kmajor(uint32_t base) { return umma::sdesc_sw128(base, 16, 1024); }
+__device__ __forceinline__ uint64_t mnmajor(uint32_t base) { return umma::sdesc_sw128(base, KT * 128, 1024); }
+__device__ __forceinline__ uint64_t kstep(uint64_t d, int kk) { return d + (((kk >> 2) * (KT * 128) + (kk & 3) * 32) >> 4); }
+__device__ __forceinline__ uint64_t mnstep(uint64_t d, int kk) { return d + kk * (2048 >> 4); }
 __device__ __forceinline__ uint32_t bits_below(int n) {
     return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
 }
@@ -153,7 +168,7 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
     // the one before (the next one's S waits for it), hence two of these and of their barriers
     __shared__ float2 stat[2][2][MH];
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int h = 0; h < 2; ++h) {
             mbar_init(&q_full[h], 1); mbar_init(&q_empty[h], 1); mbar_init(&s_full[h], 1); mbar_init(&p_full[h], 4);
@@ -180,7 +195,7 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
         const float sc2 = a.w.scale * kLog2e;
         uint32_t gt = 0, ht = 0, hi = 0;        // tiles so far; tiles and items of this half
         bool ok = true;
-        for (int64_t item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
+        for (int item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
             Work w;
             if (!w.get(a, item) || w.t0 == w.t1) continue;
             if (h >= w.halves()) { gt += w.t1 - w.t0; continue; }
@@ -320,7 +335,7 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
         uint32_t hi[2] = {0, 0};
         bool ok = true;
         const int64_t all = static_cast<int64_t>(a.w.batch) * a.w.n_q * a.w.heads;
-        for (int64_t item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
+        for (int item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
             Work w;
             if (!w.get(a, item)) continue;
             const int nh = w.halves();
@@ -374,7 +389,7 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
             // ------------------------------------------------------------ loads
             uint32_t n = 0, gt = 0, hi[2] = {0, 0};               // stage uses, tiles, items per half
             bool ok = true;
-            for (int64_t item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
+            for (int item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
                 Work w;
                 if (!w.get(a, item) || w.t0 == w.t1) continue;
                 const int nh = w.halves();
@@ -440,76 +455,83 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                 }
             }
             if (KV8) asm volatile("cp.async.wait_all;" ::: "memory");
-        } else if (warp == 13 && lane == 0) {
+        } else if (warp == 13) {
             // ------------------------------------------------------------ MMAs
+            // The whole warp walks, so that what the MMAs take (descriptors, columns) stays in
+            // uniform registers; one elected lane issues.
             constexpr uint32_t idesc_o = umma::idesc_bf16(128, D, false, true);
-            const uint32_t qb = smem_u32(qs), sb = smem_u32(st);
-            // two walks over the same tiles: S runs one tile ahead of PV
-            Work ws, wp;
-            int64_t is = blockIdx.x, ip = blockIdx.x;
-            int ts = 0, tp = 0;
-            bool have_s, have_p;
-            auto seek = [&](Work& w, int64_t& item, int& t) {
+            const uint64_t qd = kmajor(smem_u32(qs)), kd = kmajor(smem_u32(st)), vd = mnmajor(smem_u32(st));
+            // one walk over the tiles; S runs a tile ahead of PV, which keeps what it needs of the
+            // tile before (steps, halves, first and last of its item)
+            Work w;
+            int item = blockIdx.x, t = 0, total = 0, t0 = 0, t1 = 0, nh = 0;
+            auto seek = [&]() {
+                nh = 0;
                 for (; item < a.items; item += gridDim.x)
-                    if (w.get(a, item) && w.t0 < w.t1) { t = w.t0; return true; }
-                return false;
+                    if (w.get(a, item) && w.t0 < w.t1) {
+                        t = t0 = uniform(w.t0); t1 = uniform(w.t1); total = uniform(w.kl.total); nh = uniform(w.halves());
+                        return;
+                    }
             };
-            have_s = seek(ws, is, ts);
-            have_p = seek(wp, ip, tp);
-            uint32_t gs = 0, gp = 0;                              // tiles of the two walks
-            uint32_t qi[2] = {0, 0}, oi[2] = {0, 0}, pi[2] = {0, 0};
-            bool ok = true, k_ready = false;
-            auto issue_s = [&](int h) {                           // S(ts) of half h
-                if (!have_s || h >= ws.halves()) return;
-                const uint32_t n = 2 * gs;
-                if (!k_ready) {
-                    if (!(ok = spin_or_abort(&kv_full[n % STAGES], (n / STAGES) & 1, &abort_flag, a.status))) return;
-                    k_ready = true;
-                }
-                if (ts == ws.t0 && !(ok = spin_or_abort(&q_full[h], qi[h] & 1, &abort_flag, a.status))) return;
+            uint32_t gs = 0, gp = 0, qi[2] = {0, 0}, oi[2] = {0, 0}, pi[2] = {0, 0};
+            bool ok = true;
+            auto issue_s = [&](int h) {                           // S(t) of half h
+                if (!ok || h >= nh) return;
+                const uint32_t s = (2 * gs) % STAGES;
+                if (h == 0 && !(ok = spin_or_abort(&kv_full[s], (2 * gs / STAGES) & 1, &abort_flag, a.status))) return;
+                if (t == t0 && !(ok = spin_or_abort(&q_full[h], qi[h] & 1, &abort_flag, a.status))) return;
                 umma::fence_after();
-                const uint32_t idesc_s = umma::idesc_bf16(128, ws.cols(ts), false, false);
-                const uint32_t kb = sb + (n % STAGES) * Sh::TILE;
+                const uint32_t idesc_s = umma::idesc_bf16(128, min(KT, (total - t * KT + 15) & ~15), false, false);
+                const uint64_t qh = qd + h * (Sh::TILE >> 4), kb = kd + s * (Sh::TILE >> 4);
+                const bool last = t + 1 == t1;
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    umma::mma_bf16_ss(tmem + 128 * h, kmajor(qb + h * Sh::TILE, kk), kmajor(kb, kk), idesc_s, kk > 0);
-                umma::commit(&s_full[h]);
-                if (ts + 1 == ws.t1) { umma::commit(&q_empty[h]); ++qi[h]; }
-                if (h == ws.halves() - 1) umma::commit(&kv_empty[n % STAGES]);
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        umma::mma_bf16_ss(tmem + 128 * h, kstep(qh, kk), kstep(kb, kk), idesc_s, kk > 0);
+                    umma::commit(&s_full[h]);
+                    if (last) umma::commit(&q_empty[h]);
+                    if (h == nh - 1) umma::commit(&kv_empty[s]);
+                }
+                __syncwarp();
+                if (last) ++qi[h];
             };
-            auto next_s = [&]() {
-                if (!have_s) return;
+            seek();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) issue_s(h);
+            while (ok && nh > 0) {
+                const int steps = min(KT / 16, (total - t * KT + 15) >> 4), nhp = nh;
+                const bool first = t == t0, last = t + 1 == t1;
+                const uint32_t s = (2 * gp + 1) % STAGES;
+                const uint64_t vb = vd + s * (Sh::TILE >> 4);
                 ++gs;
-                k_ready = false;
-                if (++ts == ws.t1) { is += gridDim.x; have_s = seek(ws, is, ts); }
-            };
-            for (int h = 0; ok && h < 2; ++h) issue_s(h);
-            next_s();
-            while (ok && have_p) {
-                const uint32_t n = 2 * gp + 1;
-                const int steps = wp.cols(tp) >> 4;
-                const bool first = tp == wp.t0, last = tp + 1 == wp.t1;
-                bool v_ready = false;
-                for (int h = 0; ok && h < 2; ++h) {
-                    if (h < wp.halves()) {
+                if (++t == t1) { item += gridDim.x; seek(); }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (ok && h < nhp) {
                         if (!(ok = spin_or_abort(&p_full[h], pi[h] & 1, &abort_flag, a.status))) break;
                         ++pi[h];
-                        if (!v_ready && !(ok = spin_or_abort(&kv_full[n % STAGES], (n / STAGES) & 1, &abort_flag, a.status))) break;
-                        v_ready = true;
+                        if (h == 0 && !(ok = spin_or_abort(&kv_full[s], ((2 * gp + 1) / STAGES) & 1, &abort_flag, a.status))) break;
                         if (first && oi[h] > 0 && !(ok = spin_or_abort(&o_empty[h], (oi[h] - 1) & 1, &abort_flag, a.status))) break;
                         umma::fence_after();
-                        const uint32_t vb = sb + (n % STAGES) * Sh::TILE;
-                        for (int kk = 0; kk < steps; ++kk)
-                            umma::mma_bf16_ts(tmem + 256 + 128 * h, tmem + 128 * h + 8 * kk, mnmajor(vb, kk), idesc_o,
-                                              (!first || kk > 0) ? 1u : 0u);
-                        if (last) { umma::commit(&o_full[h]); ++oi[h]; }
-                        if (h == wp.halves() - 1) umma::commit(&kv_empty[n % STAGES]);
+                        const uint32_t to = tmem + 256 + 128 * h, tp = tmem + 128 * h;
+                        if (elect_one()) {
+                            if (steps == KT / 16) {
+#pragma unroll
+                                for (int kk = 0; kk < KT / 16; ++kk)
+                                    umma::mma_bf16_ts(to, tp + 8 * kk, mnstep(vb, kk), idesc_o, (!first || kk > 0) ? 1u : 0u);
+                            } else {
+                                for (int kk = 0; kk < steps; ++kk)
+                                    umma::mma_bf16_ts(to, tp + 8 * kk, mnstep(vb, kk), idesc_o, (!first || kk > 0) ? 1u : 0u);
+                            }
+                            if (last) umma::commit(&o_full[h]);
+                            if (h == nhp - 1) umma::commit(&kv_empty[s]);
+                        }
+                        __syncwarp();
+                        if (last) ++oi[h];
                     }
                     issue_s(h);
                 }
-                next_s();
                 ++gp;
-                if (++tp == wp.t1) { ip += gridDim.x; have_p = seek(wp, ip, tp); }
             }
         }
     }
@@ -569,7 +591,7 @@ cudaError_t launch(const WindowArgs& w, cudaStream_t st) {
     a.w = w;
     a.status = w.status;
     a.tiles = static_cast<int>((static_cast<int64_t>(w.n_q) * w.heads + 2 * MH - 1) / (2 * MH));
-    a.items = static_cast<int64_t>(w.batch) * a.tiles * w.splits;
+    a.items = w.batch * a.tiles * w.splits;    // fewer than 2^31 pairs, and parts only where tiles are few
     a.cap = w.cap;
     const void* k = w.k;
     const void* v = w.v;
@@ -598,7 +620,7 @@ cudaError_t launch(const WindowArgs& w, cudaStream_t st) {
         return cudaErrorInvalidValue;
     const cudaError_t e = cudaFuncSetAttribute(window_tile_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
     if (e != cudaSuccess) return e;
-    const int64_t grid = a.items < num_sms() ? a.items : num_sms();
+    const int grid = a.items < num_sms() ? a.items : num_sms();
     window_tile_kernel<D, KV8><<<static_cast<unsigned>(grid), NT, Sh::SMEM, st>>>(qm, km, vm, km16, vm16, a);
     return cudaGetLastError();
 }
