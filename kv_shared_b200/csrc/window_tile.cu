@@ -43,7 +43,10 @@ namespace {
 constexpr int KT = 128;                         // keys per tile
 constexpr int MH = 128;                         // pairs per half
 constexpr int NT = 512;
-constexpr int STAGES = 4;                       // K and V tiles in flight, K(t) at 2t, V(t) at 2t + 1
+constexpr int STAGES = 3;                       // K and V tiles in flight, K(t) at 2t, V(t) at 2t + 1
+constexpr int QSLOTS = 3;                       // halves of Q held: an item's two and the next one's first
+constexpr int ST_ROWS = 32;                     // O rows that a warp stages at a time, 64 columns wide
+constexpr int ST_BYTES = ST_ROWS * 128;
 constexpr int SC_SLOTS = 4;                     // tiles whose scales are held (at most 3 are live)
 constexpr float kLag = 8.f;                     // log2 units the reference may trail the maximum by
 constexpr uint32_t kPolyGroups = 0x11;          // of 8 groups of 4 columns: which take the FMA pipe
@@ -54,7 +57,7 @@ struct Shape {
     static constexpr int BOXES = D / 64;                       // 64-column swizzled boxes per tile
     static constexpr int BOX = KT * 128;                       // bytes of a box
     static constexpr int TILE = BOXES * BOX;
-    static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + SC_SLOTS * 2 * KT * 4;
+    static constexpr int SMEM = 1024 + (QSLOTS + STAGES) * TILE + 4 * ST_BYTES + SC_SLOTS * 2 * KT * 4;
 };
 
 struct TileArgs {
@@ -153,14 +156,16 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                                                            const __grid_constant__ CUtensorMap vmap,
                                                            const __grid_constant__ CUtensorMap kmap16,
                                                            const __grid_constant__ CUtensorMap vmap16,
+                                                           const __grid_constant__ CUtensorMap omap,
                                                            const __grid_constant__ TileArgs a) {
     using Sh = Shape<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* qs = smem;                                        // Q of halves 0, 1
-    uint8_t* st = smem + 2 * Sh::TILE;                         // K and V stages
-    float* ring = reinterpret_cast<float*>(st + STAGES * Sh::TILE);       // [SC_SLOTS][2][KT] scales (e4m3)
-    __shared__ uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], s_full[2], p_full[2], o_full[2],
+    uint8_t* qs = smem;                                        // Q slots
+    uint8_t* st = qs + QSLOTS * Sh::TILE;                      // K and V stages
+    uint8_t* so = st + STAGES * Sh::TILE;                      // O on its way out
+    float* ring = reinterpret_cast<float*>(so + 4 * ST_BYTES); // [SC_SLOTS][2][KT] scales (e4m3)
+    __shared__ uint64_t q_full[QSLOTS], q_empty[QSLOTS], kv_full[STAGES], kv_empty[STAGES], s_full[2], p_full[2], o_full[2],
         o_empty[2], st_full[2][2], sc_full[SC_SLOTS];
     __shared__ uint32_t tmem_base;
     __shared__ volatile int abort_flag;
@@ -171,10 +176,11 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int h = 0; h < 2; ++h) {
-            mbar_init(&q_full[h], 1); mbar_init(&q_empty[h], 1); mbar_init(&s_full[h], 1); mbar_init(&p_full[h], 4);
+            mbar_init(&s_full[h], 1); mbar_init(&p_full[h], 4);
             mbar_init(&o_full[h], 1); mbar_init(&o_empty[h], 4);
             mbar_init(&st_full[0][h], 4); mbar_init(&st_full[1][h], 4);
         }
+        for (int s = 0; s < QSLOTS; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 1); }
         for (int s = 0; s < STAGES; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
         for (int s = 0; s < SC_SLOTS; ++s) mbar_init(&sc_full[s], 32);
         fence_mbar_init();
@@ -353,27 +359,51 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                 umma::fence_after();
                 const float2 ml = stat[hi[h] & 1][h][m_row];
                 const float inv = a.w.splits == 1 ? 1.f / ml.y : 1.f;
+                // a warp whose 32 pairs are all in use hands its rows to TMA through shared memory
+                // (whole lines; stored by the threads, a row each, they took three times as long)
+                const bool staged = a.w.splits == 1 && w.f0 + MH * h + quarter * 32 + 31 <= w.f_last;
+                uint8_t* sw = so + quarter * ST_BYTES;
 #pragma unroll
                 for (int d = 0; d < D; d += 32) {
                     uint32_t o[32];
                     umma::tmem_ld32(tmem + lanes + 256 + 128 * h + d, o);
                     umma::tmem_ld_wait();
                     if (d + 32 == D) warp_arrive(&o_empty[h]);
-                    if (mine) {
-                        if (a.w.splits == 1) {
-                            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.w.o) + flat * D + d);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                dst[j] = make_uint4(
-                                    pack_bf16(__uint_as_float(o[8 * j]) * inv, __uint_as_float(o[8 * j + 1]) * inv),
-                                    pack_bf16(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv),
-                                    pack_bf16(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv),
-                                    pack_bf16(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv));
-                        } else {
+                    if (a.w.splits > 1) {
+                        if (mine) {
                             uint4* dst = reinterpret_cast<uint4*>(a.w.part_o + at * D + d);
 #pragma unroll
                             for (int j = 0; j < 8; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                         }
+                        continue;
+                    }
+                    uint4 x[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x[j] = make_uint4(pack_bf16(__uint_as_float(o[8 * j]) * inv, __uint_as_float(o[8 * j + 1]) * inv),
+                                          pack_bf16(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv),
+                                          pack_bf16(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv),
+                                          pack_bf16(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv));
+                    if (staged) {
+                        if (d % 64 == 0) {                       // the copy before has read the rows
+                            if (lane == 0) bulk_wait_read<0>();
+                            __syncwarp();
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4*>(sw + lane * 128 + ((((d % 64) / 8 + j) ^ (lane & 7)) << 4)) = x[j];
+                        if (d % 64 == 32) {
+                            umma::fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tma_store_2d(&omap, sw, d - 32, static_cast<int>(flat));
+                                bulk_commit();
+                            }
+                        }
+                    } else if (mine) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.w.o) + flat * D + d);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) dst[j] = x[j];
                     }
                 }
                 if (mine) {
@@ -383,17 +413,34 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                 ++hi[h];
             }
         }
+        if (lane == 0) bulk_wait_read<0>();
     } else {
         regs_dec<56>();
         if (warp == 12 && (KV8 || lane == 0)) {
             // ------------------------------------------------------------ loads
-            uint32_t n = 0, gt = 0, hi[2] = {0, 0};               // stage uses, tiles, items per half
+            uint32_t n = 0, gt = 0, qn = 0;                       // stage uses, tiles, Q slot uses
             bool ok = true;
+            auto load_q = [&](const Work& w, int h) {
+                const uint32_t s = qn % QSLOTS;
+                bool go = true;
+                if (lane == 0) {
+                    if (qn >= QSLOTS) go = wait_or_abort(&q_empty[s], (qn / QSLOTS - 1) & 1, &abort_flag, a.status);
+                    if (go) {
+                        const int row = w.b * a.w.n_q * a.w.heads + w.f0 + MH * h;
+                        mbar_arrive_expect_tx(&q_full[s], Sh::TILE);
+                        for (int c = 0; c < Sh::BOXES; ++c)
+                            tma_load_2d(qs + s * Sh::TILE + c * Sh::BOX, &qmap, &q_full[s], 64 * c, row);
+                    }
+                }
+                ++qn;
+                return KV8 ? __shfl_sync(0xffffffffu, static_cast<int>(go), 0) != 0 : go;
+            };
             for (int item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
                 Work w;
                 if (!w.get(a, item) || w.t0 == w.t1) continue;
                 const int nh = w.halves();
                 const int krow = static_cast<int>(w.b * a.cap);
+                if (!(ok = load_q(w, 0))) break;
                 for (int t = w.t0; ok && t < w.t1; ++t, ++gt) {
                     const int u0 = t * KT, groups = w.cols(t) >> 4;
                     for (int kv = 0; kv < 2; ++kv, ++n) {
@@ -434,22 +481,7 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                                 }
                                 cp_async_arrive_noinc(&sc_full[gt % SC_SLOTS]);
                             }
-                            if (t == w.t0) {
-                                for (int h = 0; ok && h < nh; ++h) {
-                                    if (lane == 0) {
-                                        if (hi[h] > 0) ok = wait_or_abort(&q_empty[h], (hi[h] - 1) & 1, &abort_flag, a.status);
-                                        if (ok) {
-                                            const int row = w.b * a.w.n_q * a.w.heads + w.f0 + MH * h;
-                                            mbar_arrive_expect_tx(&q_full[h], Sh::TILE);
-                                            for (int c = 0; c < Sh::BOXES; ++c)
-                                                tma_load_2d(qs + h * Sh::TILE + c * Sh::BOX, &qmap, &q_full[h], 64 * c, row);
-                                        }
-                                    }
-                                    if (KV8) ok = __shfl_sync(0xffffffffu, ok, 0);
-                                    ++hi[h];
-                                }
-                                if (!ok) break;
-                            }
+                            if (t == w.t0 && nh == 2 && !(ok = load_q(w, 1))) break;
                         }
                     }
                 }
@@ -473,27 +505,27 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                         return;
                     }
             };
-            uint32_t gs = 0, gp = 0, qi[2] = {0, 0}, oi[2] = {0, 0}, pi[2] = {0, 0};
+            uint32_t gs = 0, gp = 0, qn = 0, oi[2] = {0, 0}, pi[2] = {0, 0};
             bool ok = true;
             auto issue_s = [&](int h) {                           // S(t) of half h
                 if (!ok || h >= nh) return;
                 const uint32_t s = (2 * gs) % STAGES;
                 if (h == 0 && !(ok = spin_or_abort(&kv_full[s], (2 * gs / STAGES) & 1, &abort_flag, a.status))) return;
-                if (t == t0 && !(ok = spin_or_abort(&q_full[h], qi[h] & 1, &abort_flag, a.status))) return;
+                const uint32_t qslot = (qn + h) % QSLOTS;
+                if (t == t0 && !(ok = spin_or_abort(&q_full[qslot], ((qn + h) / QSLOTS) & 1, &abort_flag, a.status))) return;
                 umma::fence_after();
                 const uint32_t idesc_s = umma::idesc_bf16(128, min(KT, (total - t * KT + 15) & ~15), false, false);
-                const uint64_t qh = qd + h * (Sh::TILE >> 4), kb = kd + s * (Sh::TILE >> 4);
+                const uint64_t qh = qd + qslot * (Sh::TILE >> 4), kb = kd + s * (Sh::TILE >> 4);
                 const bool last = t + 1 == t1;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
                         umma::mma_bf16_ss(tmem + 128 * h, kstep(qh, kk), kstep(kb, kk), idesc_s, kk > 0);
                     umma::commit(&s_full[h]);
-                    if (last) umma::commit(&q_empty[h]);
+                    if (last) umma::commit(&q_empty[qslot]);
                     if (h == nh - 1) umma::commit(&kv_empty[s]);
                 }
                 __syncwarp();
-                if (last) ++qi[h];
             };
             seek();
 #pragma unroll
@@ -504,7 +536,7 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                 const uint32_t s = (2 * gp + 1) % STAGES;
                 const uint64_t vb = vd + s * (Sh::TILE >> 4);
                 ++gs;
-                if (++t == t1) { item += gridDim.x; seek(); }
+                if (++t == t1) { qn += nh; item += gridDim.x; seek(); }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (ok && h < nhp) {
@@ -611,17 +643,18 @@ cudaError_t launch(const WindowArgs& w, cudaStream_t st) {
     }
     const uint64_t pairs = static_cast<uint64_t>(w.batch) * w.n_q * w.heads, rows = static_cast<uint64_t>(w.batch) * a.cap;
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    CUtensorMap qm, km, vm, km16, vm16;
+    CUtensorMap qm, km, vm, km16, vm16, om;
     if (!make_tmap_2d(&qm, w.q, bf, 2, D, pairs, Sh::ROW, 64, MH, true) ||
         !make_tmap_2d(&km, k, bf, 2, D, rows, Sh::ROW, 64, KT, true) ||
         !make_tmap_2d(&vm, v, bf, 2, D, rows, Sh::ROW, 64, KT, true) ||
         !make_tmap_2d(&km16, k, bf, 2, D, rows, Sh::ROW, 64, 16, true) ||
-        !make_tmap_2d(&vm16, v, bf, 2, D, rows, Sh::ROW, 64, 16, true))
+        !make_tmap_2d(&vm16, v, bf, 2, D, rows, Sh::ROW, 64, 16, true) ||
+        !make_tmap_2d(&om, w.o, bf, 2, D, pairs, Sh::ROW, 64, ST_ROWS, true))
         return cudaErrorInvalidValue;
     const cudaError_t e = cudaFuncSetAttribute(window_tile_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
     if (e != cudaSuccess) return e;
     const int grid = a.items < num_sms() ? a.items : num_sms();
-    window_tile_kernel<D, KV8><<<static_cast<unsigned>(grid), NT, Sh::SMEM, st>>>(qm, km, vm, km16, vm16, a);
+    window_tile_kernel<D, KV8><<<static_cast<unsigned>(grid), NT, Sh::SMEM, st>>>(qm, km, vm, km16, vm16, om, a);
     return cudaGetLastError();
 }
 
