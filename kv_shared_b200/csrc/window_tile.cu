@@ -8,26 +8,29 @@
 // into tiles of 128, the last one as short as the list allows (a multiple of 16), so that a
 // window of 128 costs 160 columns and not 256.
 //
-// Per half and tile:  S = Q K^T into tensor memory; one thread per pair reads its row of S,
-// masks it, and forms P = 2^(S sc2 - m), which goes back over S as packed bf16 and is the A
-// operand of O += P V.  m is a reference that trails the running maximum by at most 2^8: it
-// moves, and O is rescaled in place, only when the maximum rises by more than 8 in log2
-// units, which after a row's first tile is rare; sums and O are fp32 and P keeps bf16's
-// relative rounding of 2^-8 whatever its magnitude, so nothing is lost by it.
+// Per half and tile:  S = Q K^T into tensor memory; one thread per pair reads its row of S
+// into registers, masks it, and forms P = 2^(S sc2 - m), which goes back over S as packed
+// bf16 and is the A operand of O += P V.  m is a reference that trails the running maximum by
+// at most 2^8: it moves, and O is rescaled in place, only when the maximum rises by more than
+// 8 in log2 units, which after a row's first tile is rare; sums and O are fp32 and P keeps
+// bf16's relative rounding of 2^-8 whatever its magnitude, so nothing is lost by it.
 //
 // S(i + 1) of a half is issued right behind PV(i) of the same half by the same thread: the
 // tensor pipe executes one thread's MMAs in issue order, so P(i) has been read before S(i + 1)
 // overwrites it, and S(i + 1) being complete means that O holds PV(i).  While one half's
-// threads form P the tensor cores work for the other half.
+// threads form P the tensor cores work for the other half.  P goes out in parts, so
+// that PV runs while the rest of the exponentials is formed.
 //
 // Work items (sequence, 256 pairs, part of the keys) are dealt to one persistent CTA per SM,
 // and the roles run ahead of one another across items: the next item's Q, K and V are loaded
-// and its S formed while the epilogue of this one still reads O.
+// while this one is computed, and its first S is formed while this one's O is written out.
 //
-// Roles (512 threads): warps 0-3 and 4-7 the softmax of halves 0 and 1, warps 8-11 the
-// epilogue, warp 12 the loads, one thread of warp 13 the MMAs.  The softmax threads hold a row
-// of S in registers (192 registers each, taken from the other roles).  Every wait is bounded;
-// a wait that gives up flags the status word and makes all roles leave their loops.
+// Roles (384 threads): warps 0-3 and 4-7 the softmax and the output of halves 0 and 1, warp 8
+// the loads, warps 9 and 10 the MMAs of halves 0 and 1 (a step of waits, descriptors and
+// commits is some 500 cycles of latency to its warp; in one warp the halves held each other
+// up).  The softmax threads hold a row of S in registers (208 each, taken from the others).
+// Every wait is bounded; a wait that gives up flags the status word and makes all roles leave
+// their loops.
 //
 // e4m3 caches: the codes of the rows that the call attends to are first widened to bf16
 // (exact) in the workspace; the rows' scales multiply S and P in fp32.
@@ -42,22 +45,28 @@ namespace {
 
 constexpr int KT = 128;                         // keys per tile
 constexpr int MH = 128;                         // pairs per half
-constexpr int NT = 512;
+constexpr int PART = 64, PARTS = KT / PART;     // keys of P handed over at a time
+constexpr int NT = 384;
+constexpr int NSOFT = 8;                        // softmax warps; then one for loads and two for MMAs
 constexpr int STAGES = 3;                       // K and V tiles in flight, K(t) at 2t, V(t) at 2t + 1
 constexpr int QSLOTS = 3;                       // halves of Q held: an item's two and the next one's first
-constexpr int ST_ROWS = 32;                     // O rows that a warp stages at a time, 64 columns wide
-constexpr int ST_BYTES = ST_ROWS * 128;
 constexpr int SC_SLOTS = 4;                     // tiles whose scales are held (at most 3 are live)
+constexpr int ST_BYTES = 32 * 64;               // a warp's O on its way out: 32 rows of 32 columns
 constexpr float kLag = 8.f;                     // log2 units the reference may trail the maximum by
-constexpr uint32_t kPolyGroups = 0x11;          // of 8 groups of 4 columns: which take the FMA pipe
+// tensor memory: S and P of half h at column 128 h, O at 256 + 128 h
+constexpr uint32_t kOcol = 256;
 
 template <int D>
 struct Shape {
     static constexpr int ROW = D * 2;                          // bytes of a bf16 row
     static constexpr int BOXES = D / 64;                       // 64-column swizzled boxes per tile
-    static constexpr int BOX = KT * 128;                       // bytes of a box
-    static constexpr int TILE = BOXES * BOX;
-    static constexpr int SMEM = 1024 + (QSLOTS + STAGES) * TILE + 4 * ST_BYTES + SC_SLOTS * 2 * KT * 4;
+    static constexpr int BOX = KT * 128, QBOX = MH * 128;      // bytes of a box
+    static constexpr int TILE = BOXES * BOX, QTILE = BOXES * QBOX;
+    static constexpr int BARS = 320;                          // barriers, the tensor-memory base, the abort flag
+    // all of it dynamic, so that the tiles start 1024-byte aligned without padding
+    static constexpr int OFF_KV = QSLOTS * QTILE, OFF_OUT = OFF_KV + STAGES * TILE, OFF_RING = OFF_OUT + NSOFT * ST_BYTES,
+                         OFF_BARS = OFF_RING + SC_SLOTS * 2 * KT * 4, SMEM = OFF_BARS + BARS;
+    static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
 struct TileArgs {
@@ -113,35 +122,30 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
     if (!mbar_wait(bar, parity, status)) { *abort_flag = 1; return false; }
     return true;
 }
-// the MMA warp's waits, which sit on the critical path of every handoff (whole warp)
-__device__ __forceinline__ bool spin_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
-    bool ok = mbar_test_wait(bar, parity);                     // the common case: without a look at flag or clock
-    if (__all_sync(0xffffffffu, ok)) return true;
-    if (!ok) ok = !*abort_flag && mbar_wait_spin(bar, parity, status);
-    if (__all_sync(0xffffffffu, ok)) return true;
-    *abort_flag = 1;
-    return false;
+// The same for a whole warp; in the common case, without a look at the flag or the clock.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, status));
 }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     umma::fence_before();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
+template <int R>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 // One lane of a converged warp, the same every time.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r != 0;
 }
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-template <int R>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
-template <int R>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
-
-// Descriptors of a tile's first K step (K-major with its two 64-column boxes, MN-major), of
-// which the steps differ in the address field alone: step kk at
-//   K-major  + (kk / 4) boxes + (kk % 4) 32 bytes,     MN-major  + kk 2048 bytes.
+// The warp's common value in a uniform register (a reduction leaves it there; a shuffle does not).
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+// Descriptors of a tile's first K step (K-major with its 64-column boxes, MN-major), of which
+// the steps differ in the address field alone.
 __device__ __forceinline__ uint64_t kmajor(uint32_t base) { return umma::sdesc_sw128(base, 16, 1024); }
 __device__ __forceinline__ uint64_t mnmajor(uint32_t base) { return umma::sdesc_sw128(base, KT * 128, 1024); }
 __device__ __forceinline__ uint64_t kstep(uint64_t d, int kk) { return d + (((kk >> 2) * (KT * 128) + (kk & 3) * 32) >> 4); }
@@ -156,57 +160,64 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                                                            const __grid_constant__ CUtensorMap vmap,
                                                            const __grid_constant__ CUtensorMap kmap16,
                                                            const __grid_constant__ CUtensorMap vmap16,
-                                                           const __grid_constant__ CUtensorMap omap,
                                                            const __grid_constant__ TileArgs a) {
     using Sh = Shape<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* qs = smem;                                        // Q slots
-    uint8_t* st = qs + QSLOTS * Sh::TILE;                      // K and V stages
-    uint8_t* so = st + STAGES * Sh::TILE;                      // O on its way out
-    float* ring = reinterpret_cast<float*>(so + 4 * ST_BYTES); // [SC_SLOTS][2][KT] scales (e4m3)
-    __shared__ uint64_t q_full[QSLOTS], q_empty[QSLOTS], kv_full[STAGES], kv_empty[STAGES], s_full[2], p_full[2], o_full[2],
-        o_empty[2], st_full[2][2], sc_full[SC_SLOTS];
-    __shared__ uint32_t tmem_base;
-    __shared__ volatile int abort_flag;
-    // (m, l) by item parity and half: the softmax may finish an item while the epilogue still has
-    // the one before (the next one's S waits for it), hence two of these and of their barriers
-    __shared__ float2 stat[2][2][MH];
+    uint8_t* st = smem + Sh::OFF_KV;                           // K and V stages
+    float* ring = reinterpret_cast<float*>(smem + Sh::OFF_RING);          // [SC_SLOTS][2][KT] scales (e4m3)
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + Sh::OFF_BARS);
+    uint64_t* q_empty = q_full + QSLOTS;
+    uint64_t* kv_full = q_empty + QSLOTS;
+    uint64_t* kv_empty = kv_full + STAGES;
+    uint64_t* s_full = kv_empty + STAGES;                      // [half]
+    uint64_t* p_full = s_full + 2;                             // [half][part]
+    uint64_t* o_full = p_full + 2 * PARTS;                     // [half]
+    uint64_t* sc_full = o_full + 2;                            // [SC_SLOTS]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sc_full + SC_SLOTS);
+    volatile int& abort_flag = *reinterpret_cast<volatile int*>(tmem_slot + 1);
+    static_assert((2 * QSLOTS + 2 * STAGES + 4 + 2 * PARTS + SC_SLOTS) * 8 + 8 <= Sh::BARS, "barriers fit");
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int h = 0; h < 2; ++h) {
-            mbar_init(&s_full[h], 1); mbar_init(&p_full[h], 4);
-            mbar_init(&o_full[h], 1); mbar_init(&o_empty[h], 4);
-            mbar_init(&st_full[0][h], 4); mbar_init(&st_full[1][h], 4);
+            mbar_init(&s_full[h], 1); mbar_init(&o_full[h], 1);
+            for (int i = 0; i < PARTS; ++i) mbar_init(&p_full[PARTS * h + i], 4);
         }
         for (int s = 0; s < QSLOTS; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 1); }
-        for (int s = 0; s < STAGES; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
+        for (int s = 0; s < STAGES; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 2); }
         for (int s = 0; s < SC_SLOTS; ++s) mbar_init(&sc_full[s], 32);
         fence_mbar_init();
         abort_flag = 0;
     }
-    if (warp == 13) umma::tmem_alloc(&tmem_base, 512);
+    if (warp == NSOFT + 1) umma::tmem_alloc(tmem_slot, 512);
     umma::fence_before();
     __syncthreads();
     umma::fence_after();
-    const uint32_t tmem = tmem_base;            // S/P of half h at column 128 h, O of half h at 256 + 128 h
+    const uint32_t tmem = *tmem_slot;
 
-    if (warp < 8) {
-        // ---------------------------------------------------------------- softmax
-        regs_inc<192>();
+    if (warp < NSOFT) {
+        // ---------------------------------------------------------------- softmax, output
+        regs_inc<208>();
         const int h = warp >> 2, quarter = warp & 3, m_row = quarter * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t ts = tmem + lanes + 128 * h, to = tmem + lanes + 256 + 128 * h;
+        const uint32_t ts = tmem + lanes + KT * h, to = tmem + lanes + kOcol + 128 * h;
+        uint8_t* sw = smem + Sh::OFF_OUT + warp * ST_BYTES;
         const float sc2 = a.w.scale * kLog2e;
         uint32_t gt = 0, ht = 0, hi = 0;        // tiles so far; tiles and items of this half
         bool ok = true;
+        Work w;
         for (int item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
-            Work w;
-            if (!w.get(a, item) || w.t0 == w.t1) continue;
+            if (!w.get(a, item)) continue;
+            const int f = w.f0 + MH * h + m_row;
+            const int64_t flat = static_cast<int64_t>(w.b) * a.w.n_q * a.w.heads + f;
+            const int64_t at = static_cast<int64_t>(w.split) * a.w.batch * a.w.n_q * a.w.heads + flat;
+            if (w.t0 == w.t1) {                                 // only of split keys: an empty part
+                if (f <= w.f_last) a.w.part_ml[at] = make_float2(-INFINITY, 0.f);
+                continue;
+            }
             if (h >= w.halves()) { gt += w.t1 - w.t0; continue; }
             // this pair sees list entries [lo_u, hi_u] and those below s_u
-            const int f = w.f0 + MH * h + m_row;
             int lo_u = 0, hi_u = -1, s_u = 0;
             if (f <= w.f_last) {
                 const int p = w.base + f / a.w.heads;
@@ -216,69 +227,52 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
             }
             float m = -INFINITY, l = 0.f;
             for (int t = w.t0; t < w.t1; ++t, ++gt, ++ht) {
-                if (!__all_sync(0xffffffffu, wait_or_abort(&s_full[h], ht & 1, &abort_flag, a.status))) { ok = false; break; }
+                if (!(ok = warp_wait(&s_full[h], ht & 1, &abort_flag, a.status))) break;
+                if (KV8 && !(ok = warp_wait(&sc_full[gt % SC_SLOTS], (gt / SC_SLOTS) & 1, &abort_flag, a.status))) break;
                 umma::fence_after();
-                const int u0 = t * KT, nc = (w.cols(t) + 31) >> 5;
-                // V rows of entries that hold no key may hold anything, and 0 * NaN would poison O
-                if (!KV8 && (u0 + KT > w.kl.total || (u0 < w.kl.s_pad && w.kl.s_eff < w.kl.s_pad))) {
-                    const int r = quarter * 32 + lane;
-                    const uint32_t vi = 2 * gt + 1;
-                    if (r < w.cols(t) && w.kl.row(u0 + r) < 0 &&
-                        wait_or_abort(&kv_full[vi % STAGES], (vi / STAGES) & 1, &abort_flag, a.status)) {
-                        uint8_t* vrow = st + (vi % STAGES) * Sh::TILE + r * 128;
-#pragma unroll
-                        for (int c = 0; c < Sh::BOXES * 8; ++c)
-                            *reinterpret_cast<uint4*>(vrow + (c >> 3) * Sh::BOX + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        umma::fence_proxy_async();
-                    }
-                    __syncwarp();
-                }
+                const int u0 = t * KT, cols = w.cols(t), nc = (cols + 31) >> 5;
+                const float* ksc = ring + (gt % SC_SLOTS) * 2 * KT;
                 uint32_t s[4][32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (c < nc) umma::tmem_ld32(ts + 32 * c, s[c]);
-                if (KV8 && !__all_sync(0xffffffffu, wait_or_abort(&sc_full[gt % SC_SLOTS], (gt / SC_SLOTS) & 1, &abort_flag,
-                                                                  a.status))) { ok = false; break; }
+                for (int i = 0; i < 4; ++i)
+                    if (i < nc) umma::tmem_ld32(ts + 32 * i, s[i]);
                 umma::tmem_ld_wait();
-                const float* ksc = ring + (gt % SC_SLOTS) * 2 * KT;
                 const bool masked = __any_sync(0xffffffffu, u0 < lo_u || u0 + KT - 1 > hi_u);
                 float mx = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (c < nc) {
+                for (int i = 0; i < 4; ++i)
+                    if (i < nc) {
                         if (KV8) {
 #pragma unroll
                             for (int j = 0; j < 32; j += 4) {
-                                const float4 k4 = *reinterpret_cast<const float4*>(ksc + 32 * c + j);
-                                s[c][j] = __float_as_uint(__uint_as_float(s[c][j]) * k4.x);
-                                s[c][j + 1] = __float_as_uint(__uint_as_float(s[c][j + 1]) * k4.y);
-                                s[c][j + 2] = __float_as_uint(__uint_as_float(s[c][j + 2]) * k4.z);
-                                s[c][j + 3] = __float_as_uint(__uint_as_float(s[c][j + 3]) * k4.w);
+                                const float4 k4 = *reinterpret_cast<const float4*>(ksc + 32 * i + j);
+                                s[i][j] = __float_as_uint(__uint_as_float(s[i][j]) * k4.x);
+                                s[i][j + 1] = __float_as_uint(__uint_as_float(s[i][j + 1]) * k4.y);
+                                s[i][j + 2] = __float_as_uint(__uint_as_float(s[i][j + 2]) * k4.z);
+                                s[i][j + 3] = __float_as_uint(__uint_as_float(s[i][j + 3]) * k4.w);
                             }
                         }
                         if (masked) {
-                            const int cb = u0 + 32 * c;
+                            const int cb = u0 + 32 * i;
                             const uint32_t see = (bits_below(hi_u - cb + 1) & ~bits_below(lo_u - cb)) | bits_below(s_u - cb);
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                if (!((see >> j) & 1u)) s[c][j] = 0xff800000u;              // -inf
+                                if (!((see >> j) & 1u)) s[i][j] = 0xff800000u;              // -inf
                         }
                         float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
                         for (int j = 0; j < 32; j += 4) {
-                            m0 = max3(m0, __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
-                            m1 = max3(m1, __uint_as_float(s[c][j + 2]), __uint_as_float(s[c][j + 3]));
+                            m0 = max3(m0, __uint_as_float(s[i][j]), __uint_as_float(s[i][j + 1]));
+                            m1 = max3(m1, __uint_as_float(s[i][j + 2]), __uint_as_float(s[i][j + 3]));
                         }
                         mx = max3(mx, m0, m1);
                     }
                 mx *= sc2;
-                if (mx > m) {
-                    if (m == -INFINITY) m = mx;              // nothing summed yet: l and O's row are zero
-                }
+                if (m == -INFINITY && mx > m) m = mx;           // nothing summed yet: l and O's row are zero
                 const bool move = mx > m + kLag;
                 if (__any_sync(0xffffffffu, move)) {
-                    const float c = move ? ex2(m - mx) : 1.f;
-                    l *= c;
+                    const float r = move ? ex2(m - mx) : 1.f;
+                    l *= r;
                     if (move) m = mx;
                     if (t > w.t0) {
 #pragma unroll 1
@@ -287,136 +281,100 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                             umma::tmem_ld32x16(to + d, o);
                             umma::tmem_ld_wait();
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * c);
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * r);
                             umma::tmem_st32x16(to + d, o);
                         }
-                        umma::tmem_st_wait();
                     }
                 }
                 const float off = m == -INFINITY ? 0.f : m;
                 const float2 s2 = make_float2(sc2, sc2), nm = make_float2(-off, -off);
                 float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (c < nc) {
+                for (int i = 0; i < 4; ++i) {
+                    if (i < nc) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int j = 0; j < 32; j += 4) {
-                            const float2 x0 = fma2(make_float2(__uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1])), s2, nm);
-                            const float2 x1 = fma2(make_float2(__uint_as_float(s[c][j + 2]), __uint_as_float(s[c][j + 3])), s2, nm);
-                            float2 p0, p1;
-                            if ((kPolyGroups >> (j / 4)) & 1u) {
-                                p0 = exp2_poly2(x0);
-                                p1 = exp2_poly2(x1);
-                            } else {
-                                p0 = make_float2(ex2(x0.x), ex2(x0.y));
-                                p1 = make_float2(ex2(x1.x), ex2(x1.y));
-                            }
+                            const float2 x0 = fma2(make_float2(__uint_as_float(s[i][j]), __uint_as_float(s[i][j + 1])), s2, nm);
+                            const float2 x1 = fma2(make_float2(__uint_as_float(s[i][j + 2]), __uint_as_float(s[i][j + 3])), s2, nm);
+                            float2 p0 = make_float2(ex2(x0.x), ex2(x0.y)), p1 = make_float2(ex2(x1.x), ex2(x1.y));
                             sum0 = add2(sum0, p0);
                             sum1 = add2(sum1, p1);
                             if (KV8) {
-                                const float4 v4 = *reinterpret_cast<const float4*>(ksc + KT + 32 * c + j);
+                                const float4 v4 = *reinterpret_cast<const float4*>(ksc + KT + 32 * i + j);
                                 p0.x *= v4.x; p0.y *= v4.y; p1.x *= v4.z; p1.y *= v4.w;
                             }
                             pk[j / 2] = pack_bf16(p0.x, p0.y);
                             pk[j / 2 + 1] = pack_bf16(p1.x, p1.y);
                         }
-                        umma::tmem_st32x16(ts + 16 * c, pk);
+                        umma::tmem_st32x16(ts + 16 * i, pk);
                     }
+                    if (i == 0) {
+                        // V rows of entries that hold no key may hold anything, and 0 * NaN would poison O
+                        if (!KV8 && (u0 + KT > w.kl.total || (u0 < w.kl.s_pad && w.kl.s_eff < w.kl.s_pad))) {
+                            const uint32_t vi = 2 * gt + 1;
+                            if (m_row < cols && w.kl.row(u0 + m_row) < 0 &&
+                                wait_or_abort(&kv_full[vi % STAGES], (vi / STAGES) & 1, &abort_flag, a.status)) {
+                                uint8_t* vrow = st + (vi % STAGES) * Sh::TILE + m_row * 128;
+#pragma unroll
+                                for (int c = 0; c < Sh::BOXES * 8; ++c)
+                                    *reinterpret_cast<uint4*>(vrow + (c >> 3) * Sh::BOX + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                                umma::fence_proxy_async();
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (i % (PART / 32) == PART / 32 - 1) {
+                        umma::tmem_st_wait();
+                        warp_arrive(&p_full[PARTS * h + i / (PART / 32)]);
+                    }
+                }
                 l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-                umma::tmem_st_wait();
-                warp_arrive(&p_full[h]);
             }
-            if (!ok) break;
-            stat[hi & 1][h][m_row] = make_float2(m, l);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&st_full[hi & 1][h]);
+            if (!ok || !(ok = warp_wait(&o_full[h], hi & 1, &abort_flag, a.status))) break;
             ++hi;
-        }
-    } else if (warp < 12) {
-        // ---------------------------------------------------------------- epilogue
-        regs_dec<72>();
-        const int quarter = warp & 3, m_row = quarter * 32 + lane;
-        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        uint32_t hi[2] = {0, 0};
-        bool ok = true;
-        const int64_t all = static_cast<int64_t>(a.w.batch) * a.w.n_q * a.w.heads;
-        for (int item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
-            Work w;
-            if (!w.get(a, item)) continue;
-            const int nh = w.halves();
-            for (int h = 0; h < nh; ++h) {
-                const int f = w.f0 + MH * h + m_row;
-                const int64_t flat = static_cast<int64_t>(w.b) * a.w.n_q * a.w.heads + f;
-                const int64_t at = static_cast<int64_t>(w.split) * all + flat;
-                const bool mine = f <= w.f_last;
-                if (w.t0 == w.t1) {                              // only of split keys: an empty part
-                    if (mine) a.w.part_ml[at] = make_float2(-INFINITY, 0.f);
+            umma::fence_after();
+            const float inv = a.w.splits == 1 ? 1.f / l : 1.f;
+#pragma unroll
+            for (int d = 0; d < D; d += 32) {
+                uint32_t o[32];
+                umma::tmem_ld32(to + d, o);
+                umma::tmem_ld_wait();
+                if (a.w.splits > 1) {
+                    if (f <= w.f_last) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.w.part_o + at * D + d);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    }
                     continue;
                 }
-                if (!__all_sync(0xffffffffu, wait_or_abort(&st_full[hi[h] & 1][h], (hi[h] >> 1) & 1, &abort_flag, a.status) &&
-                                                 wait_or_abort(&o_full[h], hi[h] & 1, &abort_flag, a.status))) { ok = false; break; }
-                umma::fence_after();
-                const float2 ml = stat[hi[h] & 1][h][m_row];
-                const float inv = a.w.splits == 1 ? 1.f / ml.y : 1.f;
-                // a warp whose 32 pairs are all in use hands its rows to TMA through shared memory
-                // (whole lines; stored by the threads, a row each, they took three times as long)
-                const bool staged = a.w.splits == 1 && w.f0 + MH * h + quarter * 32 + 31 <= w.f_last;
-                uint8_t* sw = so + quarter * ST_BYTES;
+                // 32 rows x 64 bytes through shared memory (16-byte chunk j of row r at j ^ (r / 2) % 4),
+                // so that each store instruction writes whole sectors
+                __syncwarp();
 #pragma unroll
-                for (int d = 0; d < D; d += 32) {
-                    uint32_t o[32];
-                    umma::tmem_ld32(tmem + lanes + 256 + 128 * h + d, o);
-                    umma::tmem_ld_wait();
-                    if (d + 32 == D) warp_arrive(&o_empty[h]);
-                    if (a.w.splits > 1) {
-                        if (mine) {
-                            uint4* dst = reinterpret_cast<uint4*>(a.w.part_o + at * D + d);
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<uint4*>(sw + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                        make_uint4(pack_bf16(__uint_as_float(o[8 * j]) * inv, __uint_as_float(o[8 * j + 1]) * inv),
+                                   pack_bf16(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv),
+                                   pack_bf16(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv),
+                                   pack_bf16(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv));
+                __syncwarp();
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                        }
-                        continue;
-                    }
-                    uint4 x[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        x[j] = make_uint4(pack_bf16(__uint_as_float(o[8 * j]) * inv, __uint_as_float(o[8 * j + 1]) * inv),
-                                          pack_bf16(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv),
-                                          pack_bf16(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv),
-                                          pack_bf16(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv));
-                    if (staged) {
-                        if (d % 64 == 0) {                       // the copy before has read the rows
-                            if (lane == 0) bulk_wait_read<0>();
-                            __syncwarp();
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<uint4*>(sw + lane * 128 + ((((d % 64) / 8 + j) ^ (lane & 7)) << 4)) = x[j];
-                        if (d % 64 == 32) {
-                            umma::fence_proxy_async();
-                            __syncwarp();
-                            if (lane == 0) {
-                                tma_store_2d(&omap, sw, d - 32, static_cast<int>(flat));
-                                bulk_commit();
-                            }
-                        }
-                    } else if (mine) {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.w.o) + flat * D + d);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) dst[j] = x[j];
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const int r = 8 * j + (lane >> 2), ch = lane & 3;
+                    const uint4 x = *reinterpret_cast<const uint4*>(sw + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+                    if (f - lane + r <= w.f_last)
+                        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.w.o) + (flat - lane + r) * D + d + 8 * ch) = x;
                 }
-                if (mine) {
-                    if (a.w.splits > 1) a.w.part_ml[at] = ml;
-                    else if (a.w.lse) a.w.lse[flat] = (ml.x + log2f(ml.y)) * kLn2;
-                }
-                ++hi[h];
+            }
+            if (f <= w.f_last) {
+                if (a.w.splits > 1) a.w.part_ml[at] = make_float2(m, l);
+                else if (a.w.lse) a.w.lse[flat] = (m + log2f(l)) * kLn2;
             }
         }
-        if (lane == 0) bulk_wait_read<0>();
     } else {
-        regs_dec<56>();
-        if (warp == 12 && (KV8 || lane == 0)) {
+        regs_dec<80>();
+        if (warp == NSOFT && (KV8 || lane == 0)) {
             // ------------------------------------------------------------ loads
             uint32_t n = 0, gt = 0, qn = 0;                       // stage uses, tiles, Q slot uses
             bool ok = true;
@@ -427,9 +385,9 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                     if (qn >= QSLOTS) go = wait_or_abort(&q_empty[s], (qn / QSLOTS - 1) & 1, &abort_flag, a.status);
                     if (go) {
                         const int row = w.b * a.w.n_q * a.w.heads + w.f0 + MH * h;
-                        mbar_arrive_expect_tx(&q_full[s], Sh::TILE);
+                        mbar_arrive_expect_tx(&q_full[s], Sh::QTILE);
                         for (int c = 0; c < Sh::BOXES; ++c)
-                            tma_load_2d(qs + s * Sh::TILE + c * Sh::BOX, &qmap, &q_full[s], 64 * c, row);
+                            tma_load_2d(qs + s * Sh::QTILE + c * Sh::QBOX, &qmap, &q_full[s], 64 * c, row);
                     }
                 }
                 ++qn;
@@ -451,7 +409,7 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                         if (!ok) break;
                         if (lane == 0) {
                             uint8_t* dst = st + s * Sh::TILE;
-                            if (u0 >= w.kl.s_pad && groups > 4) {                // one box of 128 rows
+                            if (u0 >= w.kl.s_pad && groups == KT / 16) {        // one box
                                 const CUtensorMap* map = kv ? &vmap : &kmap;
                                 const int row = krow + w.kl.lo + w.shift + u0 - w.kl.s_pad;
                                 mbar_arrive_expect_tx(&kv_full[s], Sh::TILE);
@@ -473,7 +431,7 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                                 float* slot = ring + (gt % SC_SLOTS) * 2 * KT;
                                 const int64_t seq0 = static_cast<int64_t>(w.b) * a.w.cap;
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
+                                for (int j = 0; j < KT / 32; ++j) {
                                     const int key = w.kl.row(u0 + lane + 32 * j);
                                     const int64_t src = seq0 + max(key, 0);
                                     cp_async4_zfill(slot + lane + 32 * j, a.w.k_scale + src, key >= 0);
@@ -487,14 +445,14 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                 }
             }
             if (KV8) asm volatile("cp.async.wait_all;" ::: "memory");
-        } else if (warp == 13) {
-            // ------------------------------------------------------------ MMAs
-            // The whole warp walks, so that what the MMAs take (descriptors, columns) stays in
-            // uniform registers; one elected lane issues.
+        } else if (warp == NSOFT + 1 || warp == NSOFT + 2) {
+            // ------------------------------------------------------------ MMAs of a half
+            // The whole warp walks, one elected lane issues.  S runs a tile ahead of PV, which
+            // keeps what it needs of the tile before.
+            const int h = warp - NSOFT - 1;
             constexpr uint32_t idesc_o = umma::idesc_bf16(128, D, false, true);
             const uint64_t qd = kmajor(smem_u32(qs)), kd = kmajor(smem_u32(st)), vd = mnmajor(smem_u32(st));
-            // one walk over the tiles; S runs a tile ahead of PV, which keeps what it needs of the
-            // tile before (steps, halves, first and last of its item)
+            const uint32_t tp = tmem + KT * h, to = tmem + kOcol + 128 * h;
             Work w;
             int item = blockIdx.x, t = 0, total = 0, t0 = 0, t1 = 0, nh = 0;
             auto seek = [&]() {
@@ -505,64 +463,69 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                         return;
                     }
             };
-            uint32_t gs = 0, gp = 0, qn = 0, oi[2] = {0, 0}, pi[2] = {0, 0};
+            uint32_t gs = 0, gp = 0, qn = 0, ht = 0;              // tiles of S and of PV, Q slots, PV tiles of this half
             bool ok = true;
-            auto issue_s = [&](int h) {                           // S(t) of half h
-                if (!ok || h >= nh) return;
+            auto issue_s = [&]() {
                 const uint32_t s = (2 * gs) % STAGES;
-                if (h == 0 && !(ok = spin_or_abort(&kv_full[s], (2 * gs / STAGES) & 1, &abort_flag, a.status))) return;
+                if (!(ok = warp_wait(&kv_full[s], (2 * gs / STAGES) & 1, &abort_flag, a.status))) return;
+                if (h >= nh) {                                    // the other half alone reads this stage
+                    if (lane == 0) mbar_arrive(&kv_empty[s]);
+                    return;
+                }
                 const uint32_t qslot = (qn + h) % QSLOTS;
-                if (t == t0 && !(ok = spin_or_abort(&q_full[qslot], ((qn + h) / QSLOTS) & 1, &abort_flag, a.status))) return;
+                if (t == t0 && !(ok = warp_wait(&q_full[qslot], ((qn + h) / QSLOTS) & 1, &abort_flag, a.status))) return;
                 umma::fence_after();
                 const uint32_t idesc_s = umma::idesc_bf16(128, min(KT, (total - t * KT + 15) & ~15), false, false);
-                const uint64_t qh = qd + qslot * (Sh::TILE >> 4), kb = kd + s * (Sh::TILE >> 4);
+                const uint64_t qh = qd + qslot * (Sh::QTILE >> 4), kb = kd + s * (Sh::TILE >> 4);
                 const bool last = t + 1 == t1;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
-                        umma::mma_bf16_ss(tmem + 128 * h, kstep(qh, kk), kstep(kb, kk), idesc_s, kk > 0);
+                        umma::mma_bf16_ss(tp, kstep(qh, kk), kstep(kb, kk), idesc_s, kk > 0);
                     umma::commit(&s_full[h]);
+                    umma::commit(&kv_empty[s]);
                     if (last) umma::commit(&q_empty[qslot]);
-                    if (h == nh - 1) umma::commit(&kv_empty[s]);
                 }
                 __syncwarp();
             };
             seek();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) issue_s(h);
+            if (nh > 0) issue_s();
             while (ok && nh > 0) {
-                const int steps = min(KT / 16, (total - t * KT + 15) >> 4), nhp = nh;
-                const bool first = t == t0, last = t + 1 == t1;
-                const uint32_t s = (2 * gp + 1) % STAGES;
+                const int steps = min(KT / 16, (total - t * KT + 15) >> 4);
+                const bool mine = h < nh, last = t + 1 == t1;
+                const uint32_t old = t > t0 ? 1u : 0u, s = (2 * gp + 1) % STAGES;
                 const uint64_t vb = vd + s * (Sh::TILE >> 4);
                 ++gs;
                 if (++t == t1) { qn += nh; item += gridDim.x; seek(); }
+                if (!(ok = warp_wait(&kv_full[s], ((2 * gp + 1) / STAGES) & 1, &abort_flag, a.status))) break;
+                if (mine) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (ok && h < nhp) {
-                        if (!(ok = spin_or_abort(&p_full[h], pi[h] & 1, &abort_flag, a.status))) break;
-                        ++pi[h];
-                        if (h == 0 && !(ok = spin_or_abort(&kv_full[s], ((2 * gp + 1) / STAGES) & 1, &abort_flag, a.status))) break;
-                        if (first && oi[h] > 0 && !(ok = spin_or_abort(&o_empty[h], (oi[h] - 1) & 1, &abort_flag, a.status))) break;
+                    for (int part = 0; part < PARTS; ++part) {
+                        if (!(ok = warp_wait(&p_full[PARTS * h + part], ht & 1, &abort_flag, a.status))) break;
                         umma::fence_after();
-                        const uint32_t to = tmem + 256 + 128 * h, tp = tmem + 128 * h;
+                        const int k0 = part * (PART / 16), k1 = min(steps, k0 + PART / 16);
                         if (elect_one()) {
-                            if (steps == KT / 16) {
+                            if (k1 == k0 + PART / 16) {
 #pragma unroll
-                                for (int kk = 0; kk < KT / 16; ++kk)
-                                    umma::mma_bf16_ts(to, tp + 8 * kk, mnstep(vb, kk), idesc_o, (!first || kk > 0) ? 1u : 0u);
+                                for (int kk = 0; kk < PART / 16; ++kk)
+                                    umma::mma_bf16_ts(to, tp + 8 * (k0 + kk), mnstep(vb, k0 + kk), idesc_o, k0 + kk > 0 ? 1u : old);
                             } else {
-                                for (int kk = 0; kk < steps; ++kk)
-                                    umma::mma_bf16_ts(to, tp + 8 * kk, mnstep(vb, kk), idesc_o, (!first || kk > 0) ? 1u : 0u);
+                                for (int kk = k0; kk < k1; ++kk)
+                                    umma::mma_bf16_ts(to, tp + 8 * kk, mnstep(vb, kk), idesc_o, kk > 0 ? 1u : old);
                             }
-                            if (last) umma::commit(&o_full[h]);
-                            if (h == nhp - 1) umma::commit(&kv_empty[s]);
+                            if (part == PARTS - 1) {
+                                umma::commit(&kv_empty[s]);
+                                if (last) umma::commit(&o_full[h]);
+                            }
                         }
                         __syncwarp();
-                        if (last) ++oi[h];
                     }
-                    issue_s(h);
+                    if (!ok) break;
+                    ++ht;
+                } else if (lane == 0) {
+                    mbar_arrive(&kv_empty[s]);
                 }
+                if (nh > 0) issue_s();
                 ++gp;
             }
         }
@@ -570,7 +533,7 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
     __syncwarp();
     umma::fence_before();
     __syncthreads();
-    if (warp == 13) {
+    if (warp == NSOFT + 1) {
         umma::fence_after();
         umma::tmem_dealloc(tmem, 512);
     }
@@ -643,18 +606,17 @@ cudaError_t launch(const WindowArgs& w, cudaStream_t st) {
     }
     const uint64_t pairs = static_cast<uint64_t>(w.batch) * w.n_q * w.heads, rows = static_cast<uint64_t>(w.batch) * a.cap;
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    CUtensorMap qm, km, vm, km16, vm16, om;
+    CUtensorMap qm, km, vm, km16, vm16;
     if (!make_tmap_2d(&qm, w.q, bf, 2, D, pairs, Sh::ROW, 64, MH, true) ||
         !make_tmap_2d(&km, k, bf, 2, D, rows, Sh::ROW, 64, KT, true) ||
         !make_tmap_2d(&vm, v, bf, 2, D, rows, Sh::ROW, 64, KT, true) ||
         !make_tmap_2d(&km16, k, bf, 2, D, rows, Sh::ROW, 64, 16, true) ||
-        !make_tmap_2d(&vm16, v, bf, 2, D, rows, Sh::ROW, 64, 16, true) ||
-        !make_tmap_2d(&om, w.o, bf, 2, D, pairs, Sh::ROW, 64, ST_ROWS, true))
+        !make_tmap_2d(&vm16, v, bf, 2, D, rows, Sh::ROW, 64, 16, true))
         return cudaErrorInvalidValue;
     const cudaError_t e = cudaFuncSetAttribute(window_tile_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
     if (e != cudaSuccess) return e;
     const int grid = a.items < num_sms() ? a.items : num_sms();
-    window_tile_kernel<D, KV8><<<static_cast<unsigned>(grid), NT, Sh::SMEM, st>>>(qm, km, vm, km16, vm16, om, a);
+    window_tile_kernel<D, KV8><<<static_cast<unsigned>(grid), NT, Sh::SMEM, st>>>(qm, km, vm, km16, vm16, a);
     return cudaGetLastError();
 }
 
