@@ -1,5 +1,5 @@
-// f32x2.cuh -- fp32 arithmetic on pairs and 2^x on the FMA pipe, shared by the kernels that
-// form many exponentials.
+// f32x2.cuh -- fp32 arithmetic on pairs and 2^x on the FMA pipe, for the kernels around the
+// block that form many exponentials (prefill_attn.cu has its own, with the same coefficients).
 #pragma once
 
 #include "common.cuh"
