@@ -1,0 +1,479 @@
+// accum_tile.cu -- accumulated attention weight of the cached keys on tcgen05, for bf16 and
+// e4m3 caches.
+//
+//   acc_out[j] = decay acc_in[j] + sum over rows r and heads h of
+//                exp(scale q_rh . k_j - lse_rh)            [j <= p_r]
+//
+// The log-sum-exp is known, so there is nothing to carry from key to key: S = K Q^T with the
+// keys in the MMA's M dimension puts a key's logits into one tensor-memory lane, and its total
+// is a sum inside a thread.  A CTA holds a block of keys in shared memory and streams the
+// (row, head) pairs past it, so each key is read from HBM once and each Q tile from L2 once
+// per block.  Long calls are bound by the exponential unit (one exponential per key and pair,
+// 8 cycles a warp; a quarter of them moves to the FMA pipe, 6.7), calls of a few pairs by the
+// read of K.
+//
+// Two shapes of a work item (sequence, key block, part of the pairs):
+//   wide   2 x 128 keys, pairs in tiles of 128; two threads share a key, 64 columns each
+//   narrow 4 x 128 keys, all pairs in one tile of at most 64 columns (single tokens): a thread
+//          per key, so that no thread idles and an item is worth its handovers
+// S is double-buffered (2 x 256 columns of tensor memory): the MMAs of the next tile run
+// while the exponentials of this one are formed.
+//
+// e4m3 caches: the codes are the MMA's operand as they lie in the cache.  Q goes in as a sum of
+// two e4m3 numbers, found once per call: q 2^e = hi + lo with the row's largest magnitude in
+// [128, 256).  bf16 has 8 significant bits and e4m3 4, so hi takes the upper and lo the lower
+// ones exactly, down to elements 2^-10 of the row's largest; what is lost below that is at
+// most 2^-18 of the largest, under the fp32 error of the products with it.
+//
+// Roles (640 threads): warps 0-15 exponentials, 16 the TMA loads, 17 the pairs' lse (and
+// scales), 18 and 19 the MMAs of the even and the odd 128 keys.  Every wait is bounded; a
+// wait that gives up flags the status word and makes all roles leave their loops.
+#include "common.cuh"
+#include "f32x2.cuh"
+#include "internal.h"
+#include "tcgen05.cuh"
+#include "window_keys.cuh"
+
+namespace hs2 {
+namespace {
+
+constexpr int NT = 640;
+constexpr int NEXP = 16;                        // exponential warps
+constexpr int MK = 128;                         // keys per MMA
+constexpr int NL = 4;                           // tiles whose lse are held
+constexpr int kNarrow = 64;                     // most pairs of the narrow shape
+constexpr uint32_t kPolyGroups = 0x11;          // of 8 groups of 4 columns: which take the FMA pipe
+constexpr int kSmem = 232448;
+constexpr int kBars = 16 + 16 + 4 + 4 + 8 + 8 + NL + NL + 8;
+constexpr int OFF_XCH = 1024, OFF_NL = OFF_XCH + 4 * 2 * MK * 4, OFF_TILES = OFF_NL + NL * 2 * MK * 4;
+static_assert(kBars * 8 + 8 <= OFF_XCH && OFF_TILES % 1024 == 0, "control block");
+
+struct TileArgs {
+    AccumArgs a;
+    int items, blocks, narrow;                  // batch * blocks * splits; key blocks per sequence
+    int n_cols;                                 // pairs per Q tile (a multiple of 16)
+    int k_stages, q_slots, q_bytes;
+    const float* q_scale;                       // e4m3: 2^-e of each pair
+};
+
+template <int D, bool KV8>
+struct Shape {
+    static constexpr int ROW = KV8 ? D : 2 * D;                // bytes of a K row
+    static constexpr int KBOX = ROW < 128 ? ROW : 128;         // bytes of a swizzled box's row
+    static constexpr int KBOXES = ROW / KBOX;
+    static constexpr int KTILE = MK * ROW;
+    // Q rows: bf16 in 64-column boxes; e4m3 hi then lo, a box each
+    static constexpr int QBOXES = KV8 ? 2 : D / 64;
+    static constexpr int QROW = 2 * D;
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const bool ok = !*abort_flag && mbar_wait(bar, parity, status);
+    if (!ok) *abort_flag = 1;
+    return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
+// A work item: key block [j0, end of block) of sequence b and tiles [t0, t1) of its pairs.
+struct Work {
+    int b = -1, live = 0, base = 0, j0 = 0, t0 = 0, t1 = 0, flats = 0, split = 0;
+    // false: no key of the block is in use
+    __device__ __forceinline__ bool get(const TileArgs& p, int item, int keys) {
+        const AccumArgs& a = p.a;
+        const int rest = a.splits == 1 ? item : item / a.splits;
+        split = item - rest * a.splits;
+        const int seq = rest / p.blocks;
+        j0 = (rest - seq * p.blocks) * keys;
+        if (seq != b) {
+            b = seq;
+            live = live_rows(a.n_rows, b, a.n_q);
+            base = checked_base(a.q_pos0, b, live, a.max_ctx, a.status);
+            flats = live * a.heads;
+        }
+        if (j0 >= base + live) return false;
+        const int n = (flats + p.n_cols - 1) / p.n_cols, per = a.splits == 1 ? n : (n + a.splits - 1) / a.splits;
+        // pairs at positions before the block's first key see none of its keys
+        t1 = min(n, (split + 1) * per);
+        t0 = max(min(n, split * per), max(0, j0 - base) * a.heads / p.n_cols);
+        if (t0 > t1) t0 = t1;
+        return true;
+    }
+};
+
+template <int D, bool KV8, bool NARROW>
+__global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant__ CUtensorMap kmap,
+                                                          const __grid_constant__ CUtensorMap qmap,
+                                                          const __grid_constant__ TileArgs p) {
+    using Sh = Shape<D, KV8>;
+    constexpr int MT = NARROW ? 4 : 2;                         // MMAs' worth of keys per item
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const AccumArgs& a = p.a;
+    const int KS = p.k_stages, QS = p.q_slots;
+    uint64_t* k_full = reinterpret_cast<uint64_t*>(smem);      // [16]
+    uint64_t* k_empty = k_full + 16;                           // [16]
+    uint64_t* q_full = k_empty + 16;                           // [4]
+    uint64_t* q_empty = q_full + 4;                            // [4]
+    uint64_t* s_full = q_empty + 4;                            // [buffer][MT]
+    uint64_t* s_empty = s_full + 2 * 4;                        // [buffer][MT]
+    uint64_t* nl_full = s_empty + 2 * 4;                       // [NL]
+    uint64_t* nl_empty = nl_full + NL;                         // [NL]
+    uint64_t* x_full = nl_empty + NL;                          // [4][2]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(x_full + 8);
+    volatile int& abort_flag = *reinterpret_cast<volatile int*>(tmem_slot + 1);
+    float* xch = reinterpret_cast<float*>(smem + OFF_XCH);     // [4][2][MK]
+    float* nls = reinterpret_cast<float*>(smem + OFF_NL);      // [NL][2][MK] lse in log2 units, Q scales
+    uint8_t* qs = smem + OFF_TILES;
+    uint8_t* ks = qs + QS * p.q_bytes;
+
+    const int warp = __reduce_max_sync(0xffffffffu, threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 16; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
+        for (int s = 0; s < 4; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 2); }
+        for (int s = 0; s < 8; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], NARROW ? 4 : 8); mbar_init(&x_full[s], 4); }
+        for (int s = 0; s < NL; ++s) { mbar_init(&nl_full[s], 32); mbar_init(&nl_empty[s], NEXP); }
+        fence_mbar_init();
+        abort_flag = 0;
+    }
+    if (warp == NEXP + 2) umma::tmem_alloc(tmem_slot, 512);
+    umma::fence_before();
+    __syncthreads();
+    umma::fence_after();
+    const uint32_t tmem = *tmem_slot;           // S of (buffer u, keys mt): column 256 u + mt * 256 / MT
+    Work w;
+    uint32_t step = 0;                          // Q tiles so far
+    bool ok = true;
+
+    if (warp < NEXP) {
+        // ---------------------------------------------------------------- exponentials
+        const int quarter = warp & 3, mt = NARROW ? warp >> 2 : (warp >> 2) & 1, c0 = NARROW ? 0 : 64 * (warp >> 3);
+        const uint32_t ts = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + mt * (256 / MT) + c0;
+        uint32_t it = 0;
+        const float sc2 = a.scale * kLog2e;
+        for (int item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+            if (!w.get(p, item, MK * MT)) continue;
+            const int j = w.j0 + MK * mt + 32 * quarter + lane, end = w.base + w.live;
+            const int64_t seq0 = static_cast<int64_t>(w.b) * a.cap;
+            const bool writes = j < end && c0 == 0;
+            float old = 0.f, ck = sc2;
+            if (writes && a.splits == 1 && a.acc_in) old = a.decay * a.acc_in[seq0 + j];
+            if (KV8 && j < end) ck *= __ldg(a.k_scale + seq0 + j);
+            // this key is seen by the pairs from here on
+            const int first = max(0, min(j, end - 1) - w.base) * a.heads;
+            float total = 0.f;
+            for (int t = w.t0; t < w.t1; ++t, ++step) {
+                const uint32_t u = step & 1, slot = step % NL;
+                const int f0 = t * p.n_cols + c0;
+                const int lo = first - f0, hi = min(w.flats - f0, p.n_cols - c0);       // columns lo .. hi - 1 count
+                if (!(ok = warp_wait(&s_full[4 * u + mt], (step >> 1) & 1, &abort_flag, a.status))) break;
+                if (!(ok = warp_wait(&nl_full[slot], (step / NL) & 1, &abort_flag, a.status))) break;
+                umma::fence_after();
+                const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= 64);
+                const float* nl = nls + slot * 2 * MK + c0;
+                float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+                const float2 c2 = make_float2(ck, ck);
+                uint32_t s[2][32];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (32 * i < hi) umma::tmem_ld32(ts + 256 * u + 32 * i, s[i]);
+                umma::tmem_ld_wait();
+                umma::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_empty[4 * u + mt]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (32 * i < hi) {
+                        const uint32_t see = whole ? 0xffffffffu : bits_below(hi - 32 * i) & ~bits_below(lo - 32 * i);
+#pragma unroll
+                        for (int q = 0; q < 32; q += 4) {
+                            const float4 n4 = *reinterpret_cast<const float4*>(nl + 32 * i + q);
+                            float2 ca = c2, cb = c2;
+                            if (KV8) {
+                                const float4 e4 = *reinterpret_cast<const float4*>(nl + MK + 32 * i + q);
+                                const float2 z = make_float2(0.f, 0.f);
+                                ca = fma2(c2, make_float2(e4.x, e4.y), z);
+                                cb = fma2(c2, make_float2(e4.z, e4.w), z);
+                            }
+                            const float2 x0 = fma2(make_float2(__uint_as_float(s[i][q]), __uint_as_float(s[i][q + 1])), ca, make_float2(n4.x, n4.y));
+                            const float2 x1 = fma2(make_float2(__uint_as_float(s[i][q + 2]), __uint_as_float(s[i][q + 3])), cb, make_float2(n4.z, n4.w));
+                            float2 p0, p1;
+                            if ((kPolyGroups >> (q / 4)) & 1u) {
+                                p0 = exp2_poly2(x0);
+                                p1 = exp2_poly2(x1);
+                            } else {
+                                p0 = make_float2(ex2(x0.x), ex2(x0.y));
+                                p1 = make_float2(ex2(x1.x), ex2(x1.y));
+                            }
+                            if (!whole) {                       // pairs that do not see the key, or hold anything
+                                if (!((see >> q) & 1u)) p0.x = 0.f;
+                                if (!((see >> (q + 1)) & 1u)) p0.y = 0.f;
+                                if (!((see >> (q + 2)) & 1u)) p1.x = 0.f;
+                                if (!((see >> (q + 3)) & 1u)) p1.y = 0.f;
+                            }
+                            sum0 = add2(sum0, p0);
+                            sum1 = add2(sum1, p1);
+                        }
+                    }
+                total += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&nl_empty[slot]);
+            }
+            if (!ok) break;
+            if (!NARROW && w.t0 < w.t1) {
+                // the columns' two halves: the upper one's threads hand their sums to the lower's.
+                // Four slots: a thread is at most two items ahead of the other (S has two buffers).
+                const uint32_t x = it % 4;
+                float* slot = xch + (x * 2 + mt) * MK + 32 * quarter + lane;
+                if (c0) {
+                    *slot = total;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&x_full[2 * x + mt]);
+                } else {
+                    if (!(ok = warp_wait(&x_full[2 * x + mt], (it / 4) & 1, &abort_flag, a.status))) break;
+                    total += *slot;
+                }
+                ++it;
+            }
+            if (writes) {
+                if (a.splits == 1) a.acc_out[seq0 + j] = old + total;
+                else a.part[(static_cast<int64_t>(w.split) * a.batch + w.b) * a.max_ctx + j] = total;
+            }
+        }
+    } else if (warp == NEXP) {
+        // ---------------------------------------------------------------- TMA loads
+        uint32_t kn = 0;
+        for (int item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+            if (!w.get(p, item, MK * MT) || w.t0 == w.t1) continue;
+            for (int t = w.t0; ok && t < w.t1; ++t, ++step) {
+                const uint32_t qslot = step % QS;
+                if (t == w.t0)
+                    for (int i = 0; i < MT; ++i, ++kn) {
+                        const uint32_t s = kn % KS;
+                        if (kn >= static_cast<uint32_t>(KS) &&
+                            !(ok = warp_wait(&k_empty[s], (kn / KS - 1) & 1, &abort_flag, a.status))) break;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&k_full[s], Sh::KTILE);
+                            const int row = static_cast<int>(w.b * a.cap) + w.j0 + MK * i;
+                            for (int c = 0; c < Sh::KBOXES; ++c)
+                                tma_load_2d(ks + s * Sh::KTILE + c * MK * 128, &kmap, &k_full[s], c * (KV8 ? D : 64), row);
+                        }
+                    }
+                if (!ok) break;
+                if (step >= static_cast<uint32_t>(QS) &&
+                    !(ok = warp_wait(&q_empty[qslot], (step / QS - 1) & 1, &abort_flag, a.status))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&q_full[qslot], p.n_cols * Sh::QROW);
+                    const int row = w.b * a.n_q * a.heads + t * p.n_cols;
+                    for (int c = 0; c < Sh::QBOXES; ++c)
+                        tma_load_2d(qs + qslot * p.q_bytes + c * (p.q_bytes / Sh::QBOXES), &qmap, &q_full[qslot],
+                                    c * (KV8 ? D : 64), row);
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp == NEXP + 1) {
+        // ---------------------------------------------------------------- the pairs' lse
+        for (int item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+            if (!w.get(p, item, MK * MT)) continue;
+            const int64_t flat0 = static_cast<int64_t>(w.b) * a.n_q * a.heads;
+            for (int t = w.t0; t < w.t1; ++t, ++step) {
+                const uint32_t slot = step % NL;
+                float v[4], e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int col = lane + 32 * i, f = t * p.n_cols + col;
+                    const bool in = col < p.n_cols && f < w.flats;
+                    v[i] = in ? -kLog2e * __ldg(a.lse + flat0 + f) : 0.f;
+                    e[i] = KV8 && in ? __ldg(p.q_scale + flat0 + f) : 0.f;
+                }
+                if (step >= NL && !(ok = warp_wait(&nl_empty[slot], (step / NL - 1) & 1, &abort_flag, a.status))) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    nls[slot * 2 * MK + lane + 32 * i] = v[i];
+                    if (KV8) nls[slot * 2 * MK + MK + lane + 32 * i] = e[i];
+                }
+                mbar_arrive(&nl_full[slot]);
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- MMAs
+        const int odd = warp - NEXP - 2;
+        uint32_t kn = 0;
+        const uint32_t idesc = KV8 ? umma::idesc_e4m3(MK, p.n_cols) : umma::idesc_bf16(MK, p.n_cols, false, false);
+        for (int item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+            if (!w.get(p, item, MK * MT) || w.t0 == w.t1) continue;
+            const int t0 = __reduce_max_sync(0xffffffffu, w.t0), t1 = __reduce_max_sync(0xffffffffu, w.t1);
+            for (int t = t0; ok && t < t1; ++t, ++step) {
+                const uint32_t u = step & 1, qslot = step % QS;
+                if (!(ok = warp_wait(&q_full[qslot], (step / QS) & 1, &abort_flag, a.status))) break;
+                const uint32_t qb = smem_u32(qs) + qslot * p.q_bytes;
+#pragma unroll
+                for (int i = 0; i < MT / 2; ++i) {
+                    const int mt = 2 * i + odd;
+                    const uint32_t kk0 = kn + mt, s = kk0 % KS;
+                    if (t == t0 && !(ok = warp_wait(&k_full[s], (kk0 / KS) & 1, &abort_flag, a.status))) break;
+                    if (step >= 2 && !(ok = warp_wait(&s_empty[4 * u + mt], ((step >> 1) - 1) & 1, &abort_flag, a.status))) break;
+                    umma::fence_after();
+                    const uint32_t kb = smem_u32(ks) + s * Sh::KTILE, d = tmem + 256 * u + mt * (256 / MT);
+                    if (elect_one()) {
+                        if (KV8) {
+                            const uint64_t kd = D == 128 ? umma::sdesc_sw128(kb, 16, 1024) : umma::sdesc_sw64(kb, 512);
+                            const uint64_t qh = D == 128 ? umma::sdesc_sw128(qb, 16, 1024) : umma::sdesc_sw64(qb, 512);
+                            const uint64_t ql = qh + (p.q_bytes >> 5);                  // the second half of the slot
+#pragma unroll
+                            for (int kk = 0; kk < D / 32; ++kk) umma::mma_e4m3_ss(d, kd + 2 * kk, qh + 2 * kk, idesc, kk > 0);
+#pragma unroll
+                            for (int kk = 0; kk < D / 32; ++kk) umma::mma_e4m3_ss(d, kd + 2 * kk, ql + 2 * kk, idesc, 1u);
+                        } else {
+                            const uint64_t kd = umma::sdesc_sw128(kb, 16, 1024), qd = umma::sdesc_sw128(qb, 16, 1024);
+                            const uint32_t qbox = p.q_bytes / Sh::QBOXES;
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                umma::mma_bf16_ss(d, kd + (((kk >> 2) * (MK * 128) + (kk & 3) * 32) >> 4),
+                                                  qd + (((kk >> 2) * qbox + (kk & 3) * 32) >> 4), idesc, kk > 0);
+                        }
+                        umma::commit(&s_full[4 * u + mt]);
+                        if (t + 1 == t1) umma::commit(&k_empty[s]);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (elect_one()) umma::commit(&q_empty[qslot]);
+                __syncwarp();
+            }
+            kn += MT;
+        }
+    }
+    __syncwarp();
+    umma::fence_before();
+    __syncthreads();
+    if (warp == NEXP + 2) {
+        umma::fence_after();
+        umma::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Q rows as two e4m3 numbers per element, [row][2][D], and 2^-e of each row.  16 lanes to a row.
+template <int D>
+__global__ void __launch_bounds__(256) accum_split_q_kernel(const __nv_bfloat16* __restrict__ q, int64_t rows,
+                                                            uint8_t* __restrict__ out, float* __restrict__ scale) {
+    constexpr int PER = D / 16;                                // elements of a lane: 4 or 8
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+    const int l = threadIdx.x & 15;
+    if (row >= rows) return;                                   // whole halves of a warp
+    const uint32_t half = 0xffffu << (threadIdx.x & 16);
+    float x[PER];
+    uint32_t raw[PER / 2];
+    if (PER == 8) {
+        const uint4 r = __ldg(reinterpret_cast<const uint4*>(q + row * D) + l);
+        raw[0] = r.x; raw[1] = r.y; raw[2 % (PER / 2)] = r.z; raw[3 % (PER / 2)] = r.w;
+    } else {
+        const uint2 r = __ldg(reinterpret_cast<const uint2*>(q + row * D) + l);
+        raw[0] = r.x; raw[1] = r.y;
+    }
+    float mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER / 2; ++i) {
+        x[2 * i] = __uint_as_float(raw[i] << 16);
+        x[2 * i + 1] = __uint_as_float(raw[i] & 0xffff0000u);
+        mx = fmaxf(mx, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+    }
+#pragma unroll
+    for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(half, mx, o));
+    // 2^e with mx 2^e in [128, 256); exponents kept where 2^e and 2^-e are normal numbers
+    const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;                   // mx in [2^ex, 2^(ex+1))
+    const int e = max(-120, min(120, 7 - ex));
+    const float s = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+    uint32_t hi[PER / 4], lo[PER / 4];
+#pragma unroll
+    for (int i = 0; i < PER / 2; ++i) {
+        const float y0 = x[2 * i] * s, y1 = x[2 * i + 1] * s;
+        uint16_t h, m;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(y1), "f"(y0));
+        uint32_t h2;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(h));
+        const float2 b = __half22float2(*reinterpret_cast<__half2*>(&h2));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(m) : "f"(y1 - b.y), "f"(y0 - b.x));
+        if (i & 1) {
+            hi[i / 2] |= static_cast<uint32_t>(h) << 16;
+            lo[i / 2] |= static_cast<uint32_t>(m) << 16;
+        } else {
+            hi[i / 2] = h;
+            lo[i / 2] = m;
+        }
+    }
+    uint8_t* dst = out + row * 2 * D + l * PER;
+    if (PER == 8) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[PER / 4 - 1]);
+        *reinterpret_cast<uint2*>(dst + D) = make_uint2(lo[0], lo[PER / 4 - 1]);
+    } else {
+        *reinterpret_cast<uint32_t*>(dst) = hi[0];
+        *reinterpret_cast<uint32_t*>(dst + D) = lo[0];
+    }
+    if (l == 0) scale[row] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+}
+
+template <int D, bool KV8, bool NARROW>
+cudaError_t launch(TileArgs& p, const CUtensorMap& km, const CUtensorMap& qm, cudaStream_t st) {
+    using Sh = Shape<D, KV8>;
+    const int free_bytes = kSmem - OFF_TILES;
+    p.q_bytes = (p.n_cols * Sh::QROW + 2047) / 2048 * 2048;
+    p.q_slots = 2;
+    p.k_stages = (free_bytes - p.q_slots * p.q_bytes) / Sh::KTILE;
+    if (p.k_stages > 16) p.k_stages = 16;
+    const int smem = OFF_TILES + p.q_slots * p.q_bytes + p.k_stages * Sh::KTILE;
+    const cudaError_t e = cudaFuncSetAttribute(accum_tile_kernel<D, KV8, NARROW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int grid = p.items < num_sms() ? p.items : num_sms();
+    accum_tile_kernel<D, KV8, NARROW><<<static_cast<unsigned>(grid), NT, smem, st>>>(km, qm, p);
+    return cudaGetLastError();
+}
+
+template <int D, bool KV8>
+cudaError_t launch_tile(const AccumArgs& a, cudaStream_t st) {
+    using Sh = Shape<D, KV8>;
+    TileArgs p{};
+    p.a = a;
+    const int64_t pairs = static_cast<int64_t>(a.n_q) * a.heads, all = a.batch * pairs;
+    p.narrow = pairs <= kNarrow;
+    p.n_cols = p.narrow ? static_cast<int>((pairs + 15) / 16 * 16) : MK;
+    const int keys = MK * (p.narrow ? 4 : 2);
+    p.blocks = static_cast<int>((a.max_ctx + keys - 1) / keys);
+    p.items = a.batch * p.blocks * a.splits;
+    const void* q = a.q;
+    if (KV8) {
+        uint8_t* w = static_cast<uint8_t*>(a.split_q);
+        float* scale = reinterpret_cast<float*>(w + static_cast<size_t>(all) * 2 * D);
+        accum_split_q_kernel<D><<<static_cast<unsigned>((all + 15) / 16), 256, 0, st>>>(
+            static_cast<const __nv_bfloat16*>(a.q), all, w, scale);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        q = w;
+        p.q_scale = scale;
+    }
+    const uint64_t rows = static_cast<uint64_t>(a.batch) * a.cap;
+    CUtensorMap km, qm;
+    const CUtensorMapDataType t = KV8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int eb = KV8 ? 1 : 2;
+    if (!make_tmap_2d(&km, a.k, t, eb, D, rows, Sh::ROW, Sh::KBOX / eb, MK, Sh::KBOX == 128, Sh::KBOX == 64) ||
+        !make_tmap_2d(&qm, q, t, eb, KV8 ? 2 * D : D, static_cast<uint64_t>(all), Sh::QROW, Sh::KBOX / eb,
+                      static_cast<uint32_t>(p.n_cols), Sh::KBOX == 128, Sh::KBOX == 64))
+        return cudaErrorInvalidValue;
+    return p.narrow ? launch<D, KV8, true>(p, km, qm, st) : launch<D, KV8, false>(p, km, qm, st);
+}
+
+}  // namespace
+
+cudaError_t launch_accum_tile(const AccumArgs& a, cudaStream_t st) {
+    if (a.kv_dtype == HS2_E4M3) return a.head_dim == 128 ? launch_tile<128, true>(a, st) : launch_tile<64, true>(a, st);
+    return a.head_dim == 128 ? launch_tile<128, false>(a, st) : launch_tile<64, false>(a, st);
+}
+
+}  // namespace hs2

@@ -129,7 +129,7 @@ hs2_status hs2_window_attn(const hs2_attn_desc* desc, int32_t sinks, const void*
 size_t hs2_weight_accum_workspace_size(const hs2_attn_desc* desc) {
     if (check_attn(desc) != HS2_OK) return 0;
     const int splits = plan_accum(desc->batch, desc->n_q, desc->heads, desc->kv_dtype, desc->max_ctx);
-    return kStatusBytes + accum_ws_bytes(desc->batch, splits, desc->max_ctx);
+    return kStatusBytes + accum_ws_bytes(desc->batch, desc->n_q, desc->heads, desc->head_dim, desc->kv_dtype, splits, desc->max_ctx);
 }
 
 hs2_status hs2_weight_accum(const hs2_attn_desc* desc, const void* q, const void* k, const float* k_scale,
@@ -146,7 +146,9 @@ hs2_status hs2_weight_accum(const hs2_attn_desc* desc, const void* q, const void
         if (!aligned16(p)) return HS2_ERR_INVALID_ARG;
     if (!aligned4(n_rows) || !aligned4(k_scale) || !aligned4(acc_in) || !aligned4(acc_out)) return HS2_ERR_INVALID_ARG;
     const int splits = plan_accum(desc->batch, desc->n_q, desc->heads, desc->kv_dtype, desc->max_ctx);
-    if (ws_bytes < kStatusBytes + accum_ws_bytes(desc->batch, splits, desc->max_ctx)) return HS2_ERR_WORKSPACE;
+    if (ws_bytes < kStatusBytes + accum_ws_bytes(desc->batch, desc->n_q, desc->heads, desc->head_dim, desc->kv_dtype, splits,
+                                                 desc->max_ctx))
+        return HS2_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     AccumArgs a{};
     a.batch = desc->batch; a.n_q = desc->n_q; a.heads = desc->heads; a.head_dim = desc->head_dim;
@@ -155,6 +157,7 @@ hs2_status hs2_weight_accum(const hs2_attn_desc* desc, const void* q, const void
     a.kv_dtype = desc->kv_dtype; a.lse = lse; a.scale = eff_scale(desc); a.decay = decay;
     a.acc_in = acc_in; a.acc_out = acc_out; a.splits = splits;
     if (splits > 1) a.part = reinterpret_cast<float*>(ws + kStatusBytes);
+    a.split_q = ws + kStatusBytes + accum_part_bytes(desc->batch, splits, desc->max_ctx);
     a.status = reinterpret_cast<uint32_t*>(ws);
     return from_cuda(launch_accum(a, reinterpret_cast<cudaStream_t>(stream)));
 }

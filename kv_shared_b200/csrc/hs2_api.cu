@@ -41,7 +41,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
 
 bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int elem_bytes,
                   uint64_t cols, uint64_t rows, uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows,
-                  bool swizzle128) {
+                  bool swizzle128, bool swizzle64) {
     auto enc = tmap_encoder();
     if (!enc) return false;
     (void)elem_bytes;
@@ -51,7 +51,8 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
     const cuuint32_t estr[2] = {1, 1};
     const CUresult r = enc(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
                            CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                           swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                      : (swizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE),
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }

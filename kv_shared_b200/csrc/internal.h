@@ -17,7 +17,7 @@ int num_sms();
 // `swizzle128` is set.  Returns false if the driver rejects it.
 bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int elem_bytes,
                   uint64_t cols, uint64_t rows, uint64_t row_bytes, uint32_t box_cols,
-                  uint32_t box_rows, bool swizzle128);
+                  uint32_t box_rows, bool swizzle128, bool swizzle64 = false);
 
 // ---------------------------------------------------------------- decode (n_q == 1)
 struct DecodePlan {
@@ -316,11 +316,14 @@ struct AccumArgs {
     float* acc_out;          // [B][cap]
     float* part;             // splits > 1: [split][B][max_ctx]
     int splits;              // parts the query rows are cut into
+    void* split_q;           // e4m3: [B * n_q * H][2][D] e4m3 parts of Q, then [B * n_q * H] scales
     uint32_t* status;
 };
 int plan_accum(int batch, int n_q, int heads, int kv_dtype, int64_t max_ctx);
-size_t accum_ws_bytes(int batch, int splits, int64_t max_ctx);
+size_t accum_part_bytes(int batch, int splits, int64_t max_ctx);
+size_t accum_ws_bytes(int batch, int n_q, int heads, int head_dim, int kv_dtype, int splits, int64_t max_ctx);
 cudaError_t launch_accum(const AccumArgs& a, cudaStream_t st);
+cudaError_t launch_accum_tile(const AccumArgs& a, cudaStream_t st);
 
 // ---------------------------------------------------------------- eviction
 struct EvictArgs {

@@ -1,4 +1,5 @@
-// weight_accum.cu -- accumulated attention weight of the cached keys.
+// weight_accum.cu -- accumulated attention weight of the cached keys: the fp32 kernel and
+// the join of parts.
 //
 //   acc_out[j] = decay acc_in[j] + sum over rows r and heads h of
 //                exp(scale q_rh . k_j - lse_rh)            [j <= p_r]
@@ -16,25 +17,12 @@ namespace {
 constexpr int S_KEYS = 64;                       // keys per CTA
 constexpr int S_ROWS = 32;                       // (row, head) pairs per tile
 
-// Rows of a cache or of Q as four numbers.
 __device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-    return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
-                       __uint_as_float(x.y & 0xffff0000u));
-}
-__device__ __forceinline__ float4 load4(const uint8_t* p) {
-    const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(p));
-    uint32_t lo, hi;
-    e4m3x4_to_f16x2x2(x, lo, hi);
-    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&lo)), h = __half22float2(*reinterpret_cast<__half2*>(&hi));
-    return make_float4(f.x, f.y, h.x, h.y);
-}
 
-// CUDA cores, fp32 arithmetic.  Thread (kp, qt) of 32 x 4 has keys 2 kp, 2 kp + 1 and the
+// fp32 caches on the CUDA cores.  Thread (kp, qt) of 32 x 4 has keys 2 kp, 2 kp + 1 and the
 // pairs qt + 4 i of a tile.
-template <typename TQ, typename TK, int D>
-__global__ void __launch_bounds__(128) accum_simt_kernel(AccumArgs a) {
+template <int D>
+__global__ void __launch_bounds__(128) accum_f32_kernel(AccumArgs a) {
     constexpr int LD = D + 4;
     extern __shared__ float4 sm4[];
     float* sk = reinterpret_cast<float*>(sm4);   // [64][LD]
@@ -58,21 +46,16 @@ __global__ void __launch_bounds__(128) accum_simt_kernel(AccumArgs a) {
 
     for (int i = tid; i < S_KEYS * D / 4; i += 128) {
         const int r = i / (D / 4), c = i - r * (D / 4);
-        const float4 x = j0 + r < base + live ? load4(static_cast<const TK*>(a.k) + (seq0 + j0 + r) * D + 4 * c)
+        const float4 x = j0 + r < base + live ? load4(static_cast<const float*>(a.k) + (seq0 + j0 + r) * D + 4 * c)
                                               : make_float4(0.f, 0.f, 0.f, 0.f);
         *reinterpret_cast<float4*>(sk + r * LD + 4 * c) = x;
     }
-    float ksc[2], total[2] = {0.f, 0.f};
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int j = j0 + 2 * kp + r;
-        ksc[r] = a.k_scale && j < base + live ? sc2 * a.k_scale[seq0 + j] : sc2;
-    }
+    float total[2] = {0.f, 0.f};
     for (int f0 = first; f0 < end; f0 += S_ROWS) {
         __syncthreads();
         for (int i = tid; i < S_ROWS * D / 4; i += 128) {
             const int r = i / (D / 4), c = i - r * (D / 4);
-            const float4 x = f0 + r < end ? load4(static_cast<const TQ*>(a.q) + (flat0 + f0 + r) * D + 4 * c)
+            const float4 x = f0 + r < end ? load4(static_cast<const float*>(a.q) + (flat0 + f0 + r) * D + 4 * c)
                                           : make_float4(0.f, 0.f, 0.f, 0.f);
             *reinterpret_cast<float4*>(sq + r * LD + 4 * c) = x;
         }
@@ -104,7 +87,7 @@ __global__ void __launch_bounds__(128) accum_simt_kernel(AccumArgs a) {
             const float off = s_lse[qt + 4 * i];
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-                if (j0 + 2 * kp + r <= p) total[r] += exp2f(fmaf(s[r][i], ksc[r], -off));
+                if (j0 + 2 * kp + r <= p) total[r] += exp2f(fmaf(s[r][i], sc2, -off));
         }
     }
 #pragma unroll
@@ -132,38 +115,43 @@ __global__ void __launch_bounds__(256) accum_join_kernel(AccumArgs a, int blocks
     a.acc_out[at] = a.acc_in ? fmaf(a.decay, a.acc_in[at], t) : t;
 }
 
-template <typename TQ, typename TK, int D>
-cudaError_t launch_simt(const AccumArgs& a, cudaStream_t st) {
+template <int D>
+cudaError_t launch_f32(const AccumArgs& a, cudaStream_t st) {
     constexpr int smem = (S_KEYS + S_ROWS) * (D + 4) * 4;
-    const cudaError_t e = cudaFuncSetAttribute(accum_simt_kernel<TQ, TK, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(accum_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const unsigned tiles = static_cast<unsigned>((a.max_ctx + S_KEYS - 1) / S_KEYS);
-    accum_simt_kernel<TQ, TK, D><<<dim3(tiles * a.batch, a.splits), 128, smem, st>>>(a);
+    accum_f32_kernel<D><<<dim3(tiles * a.batch, a.splits), 128, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 int plan_accum(int batch, int n_q, int heads, int kv_dtype, int64_t max_ctx) {
-    const int64_t tiles = (max_ctx + S_KEYS - 1) / S_KEYS * batch;
-    const int64_t rows = (static_cast<int64_t>(n_q) * heads + S_ROWS - 1) / S_ROWS;
-    int64_t s = 3 * num_sms() / tiles;
-    if (s > rows / 4) s = rows / 4;
-    (void)kv_dtype;
+    const bool f32 = kv_dtype == HS2_F32;
+    const int64_t keys = f32 ? S_KEYS : 256, rows = f32 ? S_ROWS : 128;
+    const int64_t blocks = (max_ctx + keys - 1) / keys * batch;
+    const int64_t tiles = (static_cast<int64_t>(n_q) * heads + rows - 1) / rows;
+    // parts of the pairs: where key blocks alone leave SMs idle, each with a few tiles of pairs
+    int64_t s = (f32 ? 3 : 1) * num_sms() / blocks;
+    const int64_t most = tiles / (f32 ? 4 : 2);
+    if (s > most) s = most;
     return s < 1 ? 1 : static_cast<int>(s);
 }
 
-size_t accum_ws_bytes(int batch, int splits, int64_t max_ctx) {
-    return splits <= 1 ? 0 : sizeof(float) * static_cast<size_t>(splits) * batch * max_ctx;
+size_t accum_part_bytes(int batch, int splits, int64_t max_ctx) {
+    const size_t n = splits <= 1 ? 0 : sizeof(float) * static_cast<size_t>(splits) * batch * max_ctx;
+    return (n + 255) & ~static_cast<size_t>(255);
+}
+
+size_t accum_ws_bytes(int batch, int n_q, int heads, int head_dim, int kv_dtype, int splits, int64_t max_ctx) {
+    const size_t q = kv_dtype == HS2_E4M3 ? static_cast<size_t>(batch) * n_q * heads * (2 * head_dim + sizeof(float)) : 0;
+    return accum_part_bytes(batch, splits, max_ctx) + q;
 }
 
 cudaError_t launch_accum(const AccumArgs& a, cudaStream_t st) {
-    cudaError_t e;
-    const bool d128 = a.head_dim == 128;
-    if (a.kv_dtype == HS2_F32) e = d128 ? launch_simt<float, float, 128>(a, st) : launch_simt<float, float, 64>(a, st);
-    else if (a.kv_dtype == HS2_BF16)
-        e = d128 ? launch_simt<__nv_bfloat16, __nv_bfloat16, 128>(a, st) : launch_simt<__nv_bfloat16, __nv_bfloat16, 64>(a, st);
-    else e = d128 ? launch_simt<__nv_bfloat16, uint8_t, 128>(a, st) : launch_simt<__nv_bfloat16, uint8_t, 64>(a, st);
+    const cudaError_t e = a.kv_dtype != HS2_F32 ? launch_accum_tile(a, st)
+                                                : (a.head_dim == 128 ? launch_f32<128>(a, st) : launch_f32<64>(a, st));
     if (e != cudaSuccess || a.splits == 1) return e;
     const int blocks = static_cast<int>((a.max_ctx + 255) / 256);
     accum_join_kernel<<<static_cast<unsigned>(blocks) * a.batch, 256, 0, st>>>(a, blocks);
