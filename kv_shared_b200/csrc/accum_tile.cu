@@ -32,6 +32,7 @@
 #include "f32x2.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
+#include "tile_sync.cuh"
 #include "window_keys.cuh"
 
 namespace hs2 {
@@ -66,21 +67,6 @@ struct Shape {
     static constexpr int QBOXES = KV8 ? 2 : D / 64;
     static constexpr int QROW = 2 * D;
 };
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    const bool ok = !*abort_flag && mbar_wait(bar, parity, status);
-    if (!ok) *abort_flag = 1;
-    return __all_sync(0xffffffffu, ok);
-}
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-__device__ __forceinline__ uint32_t bits_below(int n) {
-    return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
-}
 
 // A work item: key block [j0, end of block) of sequence b and tiles [t0, t1) of its pairs.
 struct Work {
@@ -133,7 +119,7 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
     uint8_t* qs = smem + OFF_TILES;
     uint8_t* ks = qs + QS * p.q_bytes;
 
-    const int warp = __reduce_max_sync(0xffffffffu, threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < 16; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
         for (int s = 0; s < 4; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 2); }
@@ -309,7 +295,7 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
         const uint32_t idesc = KV8 ? umma::idesc_e4m3(MK, p.n_cols) : umma::idesc_bf16(MK, p.n_cols, false, false);
         for (int item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
             if (!w.get(p, item, MK * MT) || w.t0 == w.t1) continue;
-            const int t0 = __reduce_max_sync(0xffffffffu, w.t0), t1 = __reduce_max_sync(0xffffffffu, w.t1);
+            const int t0 = uniform(w.t0), t1 = uniform(w.t1);
             for (int t = t0; ok && t < t1; ++t, ++step) {
                 const uint32_t u = step & 1, qslot = step % QS;
                 if (!(ok = warp_wait(&q_full[qslot], (step / QS) & 1, &abort_flag, a.status))) break;

@@ -38,6 +38,7 @@
 #include "f32x2.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
+#include "tile_sync.cuh"
 #include "window_keys.cuh"
 
 namespace hs2 {
@@ -117,16 +118,6 @@ struct Work {
     __device__ __forceinline__ int cols(int t) const { return min(KT, (kl.total - t * KT + 15) & ~15); }
 };
 
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
-    if (*abort_flag) return false;
-    if (!mbar_wait(bar, parity, status)) { *abort_flag = 1; return false; }
-    return true;
-}
-// The same for a whole warp; in the common case, without a look at the flag or the clock.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, status));
-}
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     umma::fence_before();
     __syncwarp();
@@ -136,23 +127,12 @@ template <int R>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
-// One lane of a converged warp, the same every time.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-// The warp's common value in a uniform register (a reduction leaves it there; a shuffle does not).
-__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
 // Descriptors of a tile's first K step (K-major with its 64-column boxes, MN-major), of which
 // the steps differ in the address field alone.
 __device__ __forceinline__ uint64_t kmajor(uint32_t base) { return umma::sdesc_sw128(base, 16, 1024); }
 __device__ __forceinline__ uint64_t mnmajor(uint32_t base) { return umma::sdesc_sw128(base, KT * 128, 1024); }
 __device__ __forceinline__ uint64_t kstep(uint64_t d, int kk) { return d + (((kk >> 2) * (KT * 128) + (kk & 3) * 32) >> 4); }
 __device__ __forceinline__ uint64_t mnstep(uint64_t d, int kk) { return d + kk * (2048 >> 4); }
-__device__ __forceinline__ uint32_t bits_below(int n) {
-    return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
-}
 
 template <int D, bool KV8>
 __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constant__ CUtensorMap qmap,
