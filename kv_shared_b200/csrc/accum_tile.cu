@@ -13,7 +13,9 @@
 // read of K.
 //
 // Two shapes of a work item (sequence, key block, part of the pairs):
-//   wide   2 x 128 keys, pairs in tiles of 128; two threads share a key, 64 columns each
+//   wide   2 x 128 keys, pairs in tiles of 128; two teams of warps take the tiles in turn, so
+//          that one's handovers fall into the other's exponentials (with both on the same
+//          tile, 64 columns a thread, everything waited at once: 3300 cycles a tile)
 //   narrow 4 x 128 keys, all pairs in one tile of at most 64 columns (single tokens): a thread
 //          per key, so that no thread idles and an item is worth its handovers
 // S is double-buffered (2 x 256 columns of tensor memory): the MMAs of the next tile run
@@ -51,7 +53,8 @@ static_assert(kBars * 8 + 8 <= OFF_XCH && OFF_TILES % 1024 == 0, "control block"
 
 struct TileArgs {
     AccumArgs a;
-    int items, blocks, narrow;                  // batch * blocks * splits; key blocks per sequence
+    WalkPlan walk;                              // (sequence, key block, part of the pairs)
+    bool narrow;
     int n_cols;                                 // pairs per Q tile (a multiple of 16)
     int k_stages, q_slots, q_bytes;
     const float* q_scale;                       // e4m3: 2^-e of each pair
@@ -68,27 +71,31 @@ struct Shape {
     static constexpr int QROW = 2 * D;
 };
 
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[32]) { umma::tmem_ld32(addr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) { umma::tmem_ld32x16(addr, r); }
+
 // A work item: key block [j0, end of block) of sequence b and tiles [t0, t1) of its pairs.
+// What depends on the sequence alone is kept from item to item.
 struct Work {
-    int b = -1, live = 0, base = 0, j0 = 0, t0 = 0, t1 = 0, flats = 0, split = 0;
+    int b = -1, live = 0, base = 0, j0 = 0, t0 = 0, t1 = 0, flats = 0, tiles = 0, per = 0, split = 0;
     // false: no key of the block is in use
-    __device__ __forceinline__ bool get(const TileArgs& p, int item, int keys) {
+    __device__ __forceinline__ bool get(const TileArgs& p, const Walk& at, int keys) {
         const AccumArgs& a = p.a;
-        const int rest = a.splits == 1 ? item : item / a.splits;
-        split = item - rest * a.splits;
-        const int seq = rest / p.blocks;
-        j0 = (rest - seq * p.blocks) * keys;
-        if (seq != b) {
-            b = seq;
+        split = at.part;
+        j0 = at.tile * keys;
+        if (at.b != b) {
+            b = at.b;
             live = live_rows(a.n_rows, b, a.n_q);
             base = checked_base(a.q_pos0, b, live, a.max_ctx, a.status);
             flats = live * a.heads;
+            tiles = (flats + p.n_cols - 1) / p.n_cols;
+            per = a.splits == 1 ? tiles : (tiles + a.splits - 1) / a.splits;
         }
         if (j0 >= base + live) return false;
-        const int n = (flats + p.n_cols - 1) / p.n_cols, per = a.splits == 1 ? n : (n + a.splits - 1) / a.splits;
+        t1 = min(tiles, (split + 1) * per);
+        t0 = min(tiles, split * per);
         // pairs at positions before the block's first key see none of its keys
-        t1 = min(n, (split + 1) * per);
-        t0 = max(min(n, split * per), max(0, j0 - base) * a.heads / p.n_cols);
+        if (j0 > base) t0 = max(t0, (j0 - base) * a.heads / p.n_cols);
         if (t0 > t1) t0 = t1;
         return true;
     }
@@ -123,8 +130,8 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
     if (threadIdx.x == 0) {
         for (int s = 0; s < 16; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
         for (int s = 0; s < 4; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 2); }
-        for (int s = 0; s < 8; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], NARROW ? 4 : 8); mbar_init(&x_full[s], 4); }
-        for (int s = 0; s < NL; ++s) { mbar_init(&nl_full[s], 32); mbar_init(&nl_empty[s], NEXP); }
+        for (int s = 0; s < 8; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], 4); mbar_init(&x_full[s], 4); }
+        for (int s = 0; s < NL; ++s) { mbar_init(&nl_full[s], 32); mbar_init(&nl_empty[s], NARROW ? NEXP : NEXP / 2); }
         fence_mbar_init();
         abort_flag = 0;
     }
@@ -139,85 +146,117 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
 
     if (warp < NEXP) {
         // ---------------------------------------------------------------- exponentials
-        const int quarter = warp & 3, mt = NARROW ? warp >> 2 : (warp >> 2) & 1, c0 = NARROW ? 0 : 64 * (warp >> 3);
-        const uint32_t ts = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + mt * (256 / MT) + c0;
+        const int quarter = warp & 3, mt = NARROW ? warp >> 2 : (warp >> 2) & 1, team = NARROW ? 0 : warp >> 3;
+        const uint32_t ts = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + mt * (256 / MT);
+        constexpr int W = NARROW ? 16 : 32;
         uint32_t it = 0;
         const float sc2 = a.scale * kLog2e;
-        for (int item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
-            if (!w.get(p, item, MK * MT)) continue;
-            const int j = w.j0 + MK * mt + 32 * quarter + lane, end = w.base + w.live;
+        // A thread's key in an item: the old total and the key's scale are loaded an item ahead.
+        struct Key {
+            int j, n;                                           // n: tiles of the item
+            bool closes, writes;                                // closes: the team of the last tile writes the totals
+            float old, ck;
+        };
+        auto key = [&](const Work& w, uint32_t step0) {
+            Key k;
+            k.j = w.j0 + MK * mt + 32 * quarter + lane;
+            k.n = w.t1 - w.t0;
+            k.closes = NARROW || (k.n == 0 ? team == 0 : static_cast<int>((step0 + k.n - 1) & 1) == team);
+            const bool live = k.j < w.base + w.live;
+            k.writes = k.closes && live;
+            const int64_t at = static_cast<int64_t>(w.b) * a.cap + k.j;
+            k.old = k.writes && a.splits == 1 && a.acc_in ? a.acc_in[at] : 0.f;
+            k.ck = KV8 && live ? __ldg(a.k_scale + at) : 1.f;
+            return k;
+        };
+        Walk pos = p.walk.at(blockIdx.x);
+        auto seek = [&](Work& w) {
+            for (; p.walk.in(pos); p.walk.next(pos))
+                if (w.get(p, pos, MK * MT)) return true;
+            return false;
+        };
+        bool more = seek(w);
+        Key k{};
+        if (more) k = key(w, 0);
+        while (ok && more) {
+            Work wn = w;
+            p.walk.next(pos);
+            more = seek(wn);
+            Key kx{};
+            if (more) kx = key(wn, step + k.n);
+            const int end = w.base + w.live, n = k.n, j = k.j;
             const int64_t seq0 = static_cast<int64_t>(w.b) * a.cap;
-            const bool writes = j < end && c0 == 0;
-            float old = 0.f, ck = sc2;
-            if (writes && a.splits == 1 && a.acc_in) old = a.decay * a.acc_in[seq0 + j];
-            if (KV8 && j < end) ck *= __ldg(a.k_scale + seq0 + j);
+            const bool closes = k.closes, writes = k.writes;
+            const float ck = sc2 * k.ck, old = a.decay * k.old;
             // this key is seen by the pairs from here on
             const int first = max(0, min(j, end - 1) - w.base) * a.heads;
             float total = 0.f;
             for (int t = w.t0; t < w.t1; ++t, ++step) {
                 const uint32_t u = step & 1, slot = step % NL;
-                const int f0 = t * p.n_cols + c0;
-                const int lo = first - f0, hi = min(w.flats - f0, p.n_cols - c0);       // columns lo .. hi - 1 count
-                if (!(ok = warp_wait(&s_full[4 * u + mt], (step >> 1) & 1, &abort_flag, a.status))) break;
-                if (!(ok = warp_wait(&nl_full[slot], (step / NL) & 1, &abort_flag, a.status))) break;
+                if (!NARROW && static_cast<int>(u) != team) continue;
+                if (!(ok = lanes_wait(lane == 0 ? &s_full[4 * u + mt] : (lane == 1 ? &nl_full[slot] : nullptr),
+                                      (lane == 0 ? step >> 1 : step / NL) & 1, &abort_flag, a.status))) break;
                 umma::fence_after();
-                const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= 64);
-                const float* nl = nls + slot * 2 * MK + c0;
-                float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
                 const float2 c2 = make_float2(ck, ck);
-                uint32_t s[2][32];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (32 * i < hi) umma::tmem_ld32(ts + 256 * u + 32 * i, s[i]);
-                umma::tmem_ld_wait();
-                umma::fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_empty[4 * u + mt]);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (32 * i < hi) {
-                        const uint32_t see = whole ? 0xffffffffu : bits_below(hi - 32 * i) & ~bits_below(lo - 32 * i);
-#pragma unroll
-                        for (int q = 0; q < 32; q += 4) {
-                            const float4 n4 = *reinterpret_cast<const float4*>(nl + 32 * i + q);
-                            float2 ca = c2, cb = c2;
-                            if (KV8) {
-                                const float4 e4 = *reinterpret_cast<const float4*>(nl + MK + 32 * i + q);
-                                const float2 z = make_float2(0.f, 0.f);
-                                ca = fma2(c2, make_float2(e4.x, e4.y), z);
-                                cb = fma2(c2, make_float2(e4.z, e4.w), z);
-                            }
-                            const float2 x0 = fma2(make_float2(__uint_as_float(s[i][q]), __uint_as_float(s[i][q + 1])), ca, make_float2(n4.x, n4.y));
-                            const float2 x1 = fma2(make_float2(__uint_as_float(s[i][q + 2]), __uint_as_float(s[i][q + 3])), cb, make_float2(n4.z, n4.w));
-                            float2 p0, p1;
-                            if ((kPolyGroups >> (q / 4)) & 1u) {
-                                p0 = exp2_poly2(x0);
-                                p1 = exp2_poly2(x1);
-                            } else {
-                                p0 = make_float2(ex2(x0.x), ex2(x0.y));
-                                p1 = make_float2(ex2(x1.x), ex2(x1.y));
-                            }
-                            if (!whole) {                       // pairs that do not see the key, or hold anything
-                                if (!((see >> q) & 1u)) p0.x = 0.f;
-                                if (!((see >> (q + 1)) & 1u)) p0.y = 0.f;
-                                if (!((see >> (q + 2)) & 1u)) p1.x = 0.f;
-                                if (!((see >> (q + 3)) & 1u)) p1.y = 0.f;
-                            }
-                            sum0 = add2(sum0, p0);
-                            sum1 = add2(sum1, p1);
-                        }
+                const int cols = min(w.flats - t * p.n_cols, p.n_cols);
+                const int lo = first - t * p.n_cols;             // columns lo .. cols - 1 count
+                // a chunk of columns at a time, in a loop: with a tile's 64 or 128 columns unrolled the
+                // registers ran out and instructions came late
+#pragma unroll 1
+                for (int c0 = 0; c0 < cols; c0 += W) {
+                    uint32_t s[W];
+                    tmem_ld(ts + 256 * u + c0, s);
+                    const bool whole = __all_sync(0xffffffffu, lo <= c0 && cols >= c0 + W);
+                    const uint32_t see = whole ? 0xffffffffu : bits_below(cols - c0) & ~bits_below(lo - c0);
+                    const float* nl = nls + slot * 2 * MK + c0;
+                    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+                    umma::tmem_ld_wait();
+                    if (c0 + W >= cols) {
+                        umma::fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s_empty[4 * u + mt]);
                     }
-                total += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+#pragma unroll
+                    for (int q = 0; q < W; q += 4) {
+                        const float4 n4 = *reinterpret_cast<const float4*>(nl + q);
+                        float2 ca = c2, cb = c2;
+                        if (KV8) {
+                            const float4 e4 = *reinterpret_cast<const float4*>(nl + MK + q);
+                            const float2 z = make_float2(0.f, 0.f);
+                            ca = fma2(c2, make_float2(e4.x, e4.y), z);
+                            cb = fma2(c2, make_float2(e4.z, e4.w), z);
+                        }
+                        const float2 x0 = fma2(make_float2(__uint_as_float(s[q]), __uint_as_float(s[q + 1])), ca, make_float2(n4.x, n4.y));
+                        const float2 x1 = fma2(make_float2(__uint_as_float(s[q + 2]), __uint_as_float(s[q + 3])), cb, make_float2(n4.z, n4.w));
+                        float2 p0, p1;
+                        if (!NARROW && ((kPolyGroups >> (q / 4)) & 1u)) {
+                            p0 = exp2_poly2(x0);
+                            p1 = exp2_poly2(x1);
+                        } else {
+                            p0 = make_float2(ex2(x0.x), ex2(x0.y));
+                            p1 = make_float2(ex2(x1.x), ex2(x1.y));
+                        }
+                        if (!whole) {                           // pairs that do not see the key, or hold anything
+                            if (!((see >> q) & 1u)) p0.x = 0.f;
+                            if (!((see >> (q + 1)) & 1u)) p0.y = 0.f;
+                            if (!((see >> (q + 2)) & 1u)) p1.x = 0.f;
+                            if (!((see >> (q + 3)) & 1u)) p1.y = 0.f;
+                        }
+                        sum0 = add2(sum0, p0);
+                        sum1 = add2(sum1, p1);
+                    }
+                    total += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&nl_empty[slot]);
             }
             if (!ok) break;
-            if (!NARROW && w.t0 < w.t1) {
-                // the columns' two halves: the upper one's threads hand their sums to the lower's.
-                // Four slots: a thread is at most two items ahead of the other (S has two buffers).
+            if (!NARROW && n > 1) {
+                // The other team's sums.  Four slots: S has a buffer per team and its MMAs are issued
+                // in order, so that a team is at most three tiles ahead of the other.
                 const uint32_t x = it % 4;
                 float* slot = xch + (x * 2 + mt) * MK + 32 * quarter + lane;
-                if (c0) {
+                if (!closes) {
                     *slot = total;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&x_full[2 * x + mt]);
@@ -231,12 +270,14 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
                 if (a.splits == 1) a.acc_out[seq0 + j] = old + total;
                 else a.part[(static_cast<int64_t>(w.split) * a.batch + w.b) * a.max_ctx + j] = total;
             }
+            w = wn;
+            k = kx;
         }
     } else if (warp == NEXP) {
         // ---------------------------------------------------------------- TMA loads
         uint32_t kn = 0;
-        for (int item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
-            if (!w.get(p, item, MK * MT) || w.t0 == w.t1) continue;
+        for (Walk at = p.walk.at(blockIdx.x); ok && p.walk.in(at); p.walk.next(at)) {
+            if (!w.get(p, at, MK * MT) || w.t0 == w.t1) continue;
             for (int t = w.t0; ok && t < w.t1; ++t, ++step) {
                 const uint32_t qslot = step % QS;
                 if (t == w.t0)
@@ -266,8 +307,8 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
         }
     } else if (warp == NEXP + 1) {
         // ---------------------------------------------------------------- the pairs' lse
-        for (int item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
-            if (!w.get(p, item, MK * MT)) continue;
+        for (Walk at = p.walk.at(blockIdx.x); ok && p.walk.in(at); p.walk.next(at)) {
+            if (!w.get(p, at, MK * MT)) continue;
             const int64_t flat0 = static_cast<int64_t>(w.b) * a.n_q * a.heads;
             for (int t = w.t0; t < w.t1; ++t, ++step) {
                 const uint32_t slot = step % NL;
@@ -293,20 +334,27 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
         const int odd = warp - NEXP - 2;
         uint32_t kn = 0;
         const uint32_t idesc = KV8 ? umma::idesc_e4m3(MK, p.n_cols) : umma::idesc_bf16(MK, p.n_cols, false, false);
-        for (int item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
-            if (!w.get(p, item, MK * MT) || w.t0 == w.t1) continue;
+        for (Walk at = p.walk.at(blockIdx.x); ok && p.walk.in(at); p.walk.next(at)) {
+            if (!w.get(p, at, MK * MT) || w.t0 == w.t1) continue;
             const int t0 = uniform(w.t0), t1 = uniform(w.t1);
             for (int t = t0; ok && t < t1; ++t, ++step) {
                 const uint32_t u = step & 1, qslot = step % QS;
-                if (!(ok = warp_wait(&q_full[qslot], (step / QS) & 1, &abort_flag, a.status))) break;
+                // lane 0: the pairs; 1, 2: S free; 3, 4: the keys
+                uint64_t* bar = lane == 0 ? &q_full[qslot] : nullptr;
+                uint32_t parity = (step / QS) & 1;
+#pragma unroll
+                for (int i = 0; i < MT / 2; ++i) {
+                    const uint32_t kx = kn + 2 * i + odd;
+                    if (lane == 1 + i && step >= 2) { bar = &s_empty[4 * u + 2 * i + odd]; parity = ((step >> 1) - 1) & 1; }
+                    if (lane == 3 + i && t == t0) { bar = &k_full[kx % KS]; parity = (kx / KS) & 1; }
+                }
+                if (!(ok = lanes_wait(bar, parity, &abort_flag, a.status))) break;
+                umma::fence_after();
                 const uint32_t qb = smem_u32(qs) + qslot * p.q_bytes;
 #pragma unroll
                 for (int i = 0; i < MT / 2; ++i) {
                     const int mt = 2 * i + odd;
-                    const uint32_t kk0 = kn + mt, s = kk0 % KS;
-                    if (t == t0 && !(ok = warp_wait(&k_full[s], (kk0 / KS) & 1, &abort_flag, a.status))) break;
-                    if (step >= 2 && !(ok = warp_wait(&s_empty[4 * u + mt], ((step >> 1) - 1) & 1, &abort_flag, a.status))) break;
-                    umma::fence_after();
+                    const uint32_t s = (kn + mt) % KS;
                     const uint32_t kb = smem_u32(ks) + s * Sh::KTILE, d = tmem + 256 * u + mt * (256 / MT);
                     if (elect_one()) {
                         if (KV8) {
@@ -327,12 +375,10 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
                         }
                         umma::commit(&s_full[4 * u + mt]);
                         if (t + 1 == t1) umma::commit(&k_empty[s]);
+                        if (i == MT / 2 - 1) umma::commit(&q_empty[qslot]);
                     }
                     __syncwarp();
                 }
-                if (!ok) break;
-                if (elect_one()) umma::commit(&q_empty[qslot]);
-                __syncwarp();
             }
             kn += MT;
         }
@@ -417,7 +463,9 @@ cudaError_t launch(TileArgs& p, const CUtensorMap& km, const CUtensorMap& qm, cu
     const int smem = OFF_TILES + p.q_slots * p.q_bytes + p.k_stages * Sh::KTILE;
     const cudaError_t e = cudaFuncSetAttribute(accum_tile_kernel<D, KV8, NARROW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int grid = p.items < num_sms() ? p.items : num_sms();
+    const int64_t items = static_cast<int64_t>(p.walk.batch) * p.walk.tiles * p.walk.parts;
+    const int grid = items < num_sms() ? static_cast<int>(items) : num_sms();
+    p.walk.step = p.walk.at(grid);
     accum_tile_kernel<D, KV8, NARROW><<<static_cast<unsigned>(grid), NT, smem, st>>>(km, qm, p);
     return cudaGetLastError();
 }
@@ -431,8 +479,9 @@ cudaError_t launch_tile(const AccumArgs& a, cudaStream_t st) {
     p.narrow = pairs <= kNarrow;
     p.n_cols = p.narrow ? static_cast<int>((pairs + 15) / 16 * 16) : MK;
     const int keys = MK * (p.narrow ? 4 : 2);
-    p.blocks = static_cast<int>((a.max_ctx + keys - 1) / keys);
-    p.items = a.batch * p.blocks * a.splits;
+    p.walk.batch = a.batch;
+    p.walk.tiles = static_cast<int>((a.max_ctx + keys - 1) / keys);
+    p.walk.parts = a.splits;
     const void* q = a.q;
     if (KV8) {
         uint8_t* w = static_cast<uint8_t*>(a.split_q);

@@ -72,8 +72,8 @@ struct Shape {
 
 struct TileArgs {
     WindowArgs w;
-    int items;                                  // batch * tiles * splits
-    int tiles;                                  // 256-pair tiles per sequence
+    WalkPlan walk;                              // (sequence, 256 pairs, part of the keys)
+    FastDiv heads;
     int64_t cap;                                // rows per sequence of the maps' K and V
     int s16;                                    // e4m3: widened sink rows per sequence
     uint32_t* status;
@@ -93,20 +93,18 @@ struct Work {
     KeyList kl;
     __device__ __forceinline__ Work() : b(-1), kl(0, 0, 1, 0) {}
     // false: no pairs in use.  t0 == t1: no keys in this part.
-    __device__ __forceinline__ bool get(const TileArgs& a, int item) {
+    __device__ __forceinline__ bool get(const TileArgs& a, const Walk& at) {
         const WindowArgs& w = a.w;
-        const int rest = w.splits == 1 ? item : item / w.splits;
-        split = item - rest * w.splits;
-        const int seq = rest / a.tiles;
-        f0 = (rest - seq * a.tiles) * 2 * MH;
-        if (seq != b) {
-            b = seq;
+        split = at.part;
+        f0 = at.tile * 2 * MH;
+        if (at.b != b) {
+            b = at.b;
             live = live_rows(w.n_rows, b, w.n_q);
             base = checked_base(w.q_pos0, b, live, w.max_ctx, a.status);
         }
         if (f0 >= live * w.heads) return false;
         f_last = min(f0 + 2 * MH - 1, live * w.heads - 1);
-        kl = KeyList(base + f0 / w.heads, base + f_last / w.heads, w.window, w.sinks);
+        kl = KeyList(base + a.heads.div(f0), base + a.heads.div(f_last), w.window, w.sinks);
         const int n = (kl.total + KT - 1) / KT, per = w.splits == 1 ? n : (n + w.splits - 1) / w.splits;
         t0 = min(n, split * per);
         t1 = min(n, t0 + per);
@@ -187,8 +185,8 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
         uint32_t gt = 0, ht = 0, hi = 0;        // tiles so far; tiles and items of this half
         bool ok = true;
         Work w;
-        for (int item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
-            if (!w.get(a, item)) continue;
+        for (Walk pos = a.walk.at(blockIdx.x); ok && a.walk.in(pos); a.walk.next(pos)) {
+            if (!w.get(a, pos)) continue;
             const int f = w.f0 + MH * h + m_row;
             const int64_t flat = static_cast<int64_t>(w.b) * a.w.n_q * a.w.heads + f;
             const int64_t at = static_cast<int64_t>(w.split) * a.w.batch * a.w.n_q * a.w.heads + flat;
@@ -200,7 +198,7 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
             // this pair sees list entries [lo_u, hi_u] and those below s_u
             int lo_u = 0, hi_u = -1, s_u = 0;
             if (f <= w.f_last) {
-                const int p = w.base + f / a.w.heads;
+                const int p = w.base + a.heads.div(f);
                 lo_u = max(p - a.w.window + 1 - w.kl.lo, 0) + w.kl.s_pad;
                 hi_u = p - w.kl.lo + w.kl.s_pad;
                 s_u = w.kl.lo > 0 ? w.kl.s_eff : min(a.w.sinks, p + 1);
@@ -373,9 +371,9 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                 ++qn;
                 return KV8 ? __shfl_sync(0xffffffffu, static_cast<int>(go), 0) != 0 : go;
             };
-            for (int item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
-                Work w;
-                if (!w.get(a, item) || w.t0 == w.t1) continue;
+            Work w;
+            for (Walk pos = a.walk.at(blockIdx.x); ok && a.walk.in(pos); a.walk.next(pos)) {
+                if (!w.get(a, pos) || w.t0 == w.t1) continue;
                 const int nh = w.halves();
                 const int krow = static_cast<int>(w.b * a.cap);
                 if (!(ok = load_q(w, 0))) break;
@@ -434,11 +432,12 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
             const uint64_t qd = kmajor(smem_u32(qs)), kd = kmajor(smem_u32(st)), vd = mnmajor(smem_u32(st));
             const uint32_t tp = tmem + KT * h, to = tmem + kOcol + 128 * h;
             Work w;
-            int item = blockIdx.x, t = 0, total = 0, t0 = 0, t1 = 0, nh = 0;
+            Walk pos = a.walk.at(blockIdx.x);
+            int t = 0, total = 0, t0 = 0, t1 = 0, nh = 0;
             auto seek = [&]() {
                 nh = 0;
-                for (; item < a.items; item += gridDim.x)
-                    if (w.get(a, item) && w.t0 < w.t1) {
+                for (; a.walk.in(pos); a.walk.next(pos))
+                    if (w.get(a, pos) && w.t0 < w.t1) {
                         t = t0 = uniform(w.t0); t1 = uniform(w.t1); total = uniform(w.kl.total); nh = uniform(w.halves());
                         return;
                     }
@@ -476,7 +475,7 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                 const uint32_t old = t > t0 ? 1u : 0u, s = (2 * gp + 1) % STAGES;
                 const uint64_t vb = vd + s * (Sh::TILE >> 4);
                 ++gs;
-                if (++t == t1) { qn += nh; item += gridDim.x; seek(); }
+                if (++t == t1) { qn += nh; a.walk.next(pos); seek(); }
                 if (!(ok = warp_wait(&kv_full[s], ((2 * gp + 1) / STAGES) & 1, &abort_flag, a.status))) break;
                 if (mine) {
 #pragma unroll
@@ -565,8 +564,13 @@ cudaError_t launch(const WindowArgs& w, cudaStream_t st) {
     TileArgs a{};
     a.w = w;
     a.status = w.status;
-    a.tiles = static_cast<int>((static_cast<int64_t>(w.n_q) * w.heads + 2 * MH - 1) / (2 * MH));
-    a.items = w.batch * a.tiles * w.splits;    // fewer than 2^31 pairs, and parts only where tiles are few
+    a.heads = FastDiv(static_cast<uint32_t>(w.heads));
+    a.walk.batch = w.batch;
+    a.walk.tiles = static_cast<int>((static_cast<int64_t>(w.n_q) * w.heads + 2 * MH - 1) / (2 * MH));
+    a.walk.parts = w.splits;
+    const int64_t items = static_cast<int64_t>(a.walk.batch) * a.walk.tiles * a.walk.parts;
+    const int grid = items < num_sms() ? static_cast<int>(items) : num_sms();
+    a.walk.step = a.walk.at(grid);
     a.cap = w.cap;
     const void* k = w.k;
     const void* v = w.v;
@@ -595,7 +599,6 @@ cudaError_t launch(const WindowArgs& w, cudaStream_t st) {
         return cudaErrorInvalidValue;
     const cudaError_t e = cudaFuncSetAttribute(window_tile_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
     if (e != cudaSuccess) return e;
-    const int grid = a.items < num_sms() ? a.items : num_sms();
     window_tile_kernel<D, KV8><<<static_cast<unsigned>(grid), NT, Sh::SMEM, st>>>(qm, km, vm, km16, vm16, a);
     return cudaGetLastError();
 }
