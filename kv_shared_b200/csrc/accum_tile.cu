@@ -75,29 +75,44 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[32]) { umma
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) { umma::tmem_ld32x16(addr, r); }
 
 // A work item: key block [j0, end of block) of sequence b and tiles [t0, t1) of its pairs.
-// What depends on the sequence alone is kept from item to item.
+// What depends on the sequence alone is kept from item to item; an item costs each role a
+// handful of instructions (a division proper is hundreds of cycles to a lone warp).
+template <bool NARROW>
 struct Work {
-    int b = -1, live = 0, base = 0, j0 = 0, t0 = 0, t1 = 0, flats = 0, tiles = 0, per = 0, split = 0;
+    static constexpr int KEYS = MK * (NARROW ? 4 : 2);
+    int b = -1, end = 0, base = 0, j0 = 0, t0 = 0, t1 = 0, flats = 0, tiles = 0, per = 0, split = 0;
     // false: no key of the block is in use
-    __device__ __forceinline__ bool get(const TileArgs& p, const Walk& at, int keys) {
+    __device__ __forceinline__ bool get(const TileArgs& p, const Walk& at) {
         const AccumArgs& a = p.a;
-        split = at.part;
-        j0 = at.tile * keys;
+        j0 = at.tile * KEYS;
         if (at.b != b) {
             b = at.b;
-            live = live_rows(a.n_rows, b, a.n_q);
+            const int live = live_rows(a.n_rows, b, a.n_q);
             base = checked_base(a.q_pos0, b, live, a.max_ctx, a.status);
+            end = base + live;
             flats = live * a.heads;
-            tiles = (flats + p.n_cols - 1) / p.n_cols;
+            tiles = (flats + MK - 1) / MK;                     // narrow: one
             per = a.splits == 1 ? tiles : (tiles + a.splits - 1) / a.splits;
         }
-        if (j0 >= base + live) return false;
-        t1 = min(tiles, (split + 1) * per);
-        t0 = min(tiles, split * per);
-        // pairs at positions before the block's first key see none of its keys
-        if (j0 > base) t0 = max(t0, (j0 - base) * a.heads / p.n_cols);
-        if (t0 > t1) t0 = t1;
+        if (j0 >= end) return false;
+        if (NARROW) {
+            t1 = tiles;
+        } else {
+            split = at.part;
+            t1 = min(tiles, (split + 1) * per);
+            t0 = min(tiles, split * per);
+            // pairs at positions before the block's first key see none of its keys
+            if (j0 > base) t0 = min(t1, max(t0, (j0 - base) * a.heads / MK));
+        }
         return true;
+    }
+};
+
+// Slot and phase of a ring's next use.
+struct Ring {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void next(uint32_t size) {
+        if (++slot == size) { slot = 0; phase ^= 1u; }
     }
 };
 
@@ -140,7 +155,7 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
     __syncthreads();
     umma::fence_after();
     const uint32_t tmem = *tmem_slot;           // S of (buffer u, keys mt): column 256 u + mt * 256 / MT
-    Work w;
+    Work<NARROW> w;
     uint32_t step = 0;                          // Q tiles so far
     bool ok = true;
 
@@ -157,12 +172,12 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
             bool closes, writes;                                // closes: the team of the last tile writes the totals
             float old, ck;
         };
-        auto key = [&](const Work& w, uint32_t step0) {
+        auto key = [&](const Work<NARROW>& w, uint32_t step0) {
             Key k;
             k.j = w.j0 + MK * mt + 32 * quarter + lane;
             k.n = w.t1 - w.t0;
             k.closes = NARROW || (k.n == 0 ? team == 0 : static_cast<int>((step0 + k.n - 1) & 1) == team);
-            const bool live = k.j < w.base + w.live;
+            const bool live = k.j < w.end;
             k.writes = k.closes && live;
             const int64_t at = static_cast<int64_t>(w.b) * a.cap + k.j;
             k.old = k.writes && a.splits == 1 && a.acc_in ? a.acc_in[at] : 0.f;
@@ -170,26 +185,26 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
             return k;
         };
         Walk pos = p.walk.at(blockIdx.x);
-        auto seek = [&](Work& w) {
+        auto seek = [&](Work<NARROW>& w) {
             for (; p.walk.in(pos); p.walk.next(pos))
-                if (w.get(p, pos, MK * MT)) return true;
+                if (w.get(p, pos)) return true;
             return false;
         };
         bool more = seek(w);
         Key k{};
         if (more) k = key(w, 0);
         while (ok && more) {
-            Work wn = w;
+            Work<NARROW> wn = w;
             p.walk.next(pos);
             more = seek(wn);
             Key kx{};
             if (more) kx = key(wn, step + k.n);
-            const int end = w.base + w.live, n = k.n, j = k.j;
+            const int n = k.n, j = k.j;
             const int64_t seq0 = static_cast<int64_t>(w.b) * a.cap;
             const bool closes = k.closes, writes = k.writes;
             const float ck = sc2 * k.ck, old = a.decay * k.old;
             // this key is seen by the pairs from here on
-            const int first = max(0, min(j, end - 1) - w.base) * a.heads;
+            const int first = max(0, min(j, w.end - 1) - w.base) * a.heads;
             float total = 0.f;
             for (int t = w.t0; t < w.t1; ++t, ++step) {
                 const uint32_t u = step & 1, slot = step % NL;
@@ -275,40 +290,40 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
         }
     } else if (warp == NEXP) {
         // ---------------------------------------------------------------- TMA loads
-        uint32_t kn = 0;
+        Ring kr, qr;
+        uint32_t kfree = KS, qfree = QS;                       // slots never used so far need no wait
         for (Walk at = p.walk.at(blockIdx.x); ok && p.walk.in(at); p.walk.next(at)) {
-            if (!w.get(p, at, MK * MT) || w.t0 == w.t1) continue;
-            for (int t = w.t0; ok && t < w.t1; ++t, ++step) {
-                const uint32_t qslot = step % QS;
+            if (!w.get(p, at) || w.t0 == w.t1) continue;
+            const int krow = static_cast<int>(w.b * a.cap) + w.j0, qrow = w.b * a.n_q * a.heads;
+            for (int t = w.t0; ok && t < w.t1; ++t) {
                 if (t == w.t0)
-                    for (int i = 0; i < MT; ++i, ++kn) {
-                        const uint32_t s = kn % KS;
-                        if (kn >= static_cast<uint32_t>(KS) &&
-                            !(ok = warp_wait(&k_empty[s], (kn / KS - 1) & 1, &abort_flag, a.status))) break;
+                    for (int i = 0; i < MT; ++i, kr.next(KS)) {
+                        if (kfree > 0) --kfree;
+                        else if (!(ok = warp_wait(&k_empty[kr.slot], kr.phase ^ 1u, &abort_flag, a.status))) break;
                         if (lane == 0) {
-                            mbar_arrive_expect_tx(&k_full[s], Sh::KTILE);
-                            const int row = static_cast<int>(w.b * a.cap) + w.j0 + MK * i;
+                            mbar_arrive_expect_tx(&k_full[kr.slot], Sh::KTILE);
                             for (int c = 0; c < Sh::KBOXES; ++c)
-                                tma_load_2d(ks + s * Sh::KTILE + c * MK * 128, &kmap, &k_full[s], c * (KV8 ? D : 64), row);
+                                tma_load_2d(ks + kr.slot * Sh::KTILE + c * MK * 128, &kmap, &k_full[kr.slot], c * (KV8 ? D : 64),
+                                            krow + MK * i);
                         }
                     }
                 if (!ok) break;
-                if (step >= static_cast<uint32_t>(QS) &&
-                    !(ok = warp_wait(&q_empty[qslot], (step / QS - 1) & 1, &abort_flag, a.status))) break;
+                if (qfree > 0) --qfree;
+                else if (!(ok = warp_wait(&q_empty[qr.slot], qr.phase ^ 1u, &abort_flag, a.status))) break;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&q_full[qslot], p.n_cols * Sh::QROW);
-                    const int row = w.b * a.n_q * a.heads + t * p.n_cols;
+                    mbar_arrive_expect_tx(&q_full[qr.slot], p.n_cols * Sh::QROW);
                     for (int c = 0; c < Sh::QBOXES; ++c)
-                        tma_load_2d(qs + qslot * p.q_bytes + c * (p.q_bytes / Sh::QBOXES), &qmap, &q_full[qslot],
-                                    c * (KV8 ? D : 64), row);
+                        tma_load_2d(qs + qr.slot * p.q_bytes + c * (p.q_bytes / Sh::QBOXES), &qmap, &q_full[qr.slot],
+                                    c * (KV8 ? D : 64), qrow + t * p.n_cols);
                 }
                 __syncwarp();
+                qr.next(QS);
             }
         }
     } else if (warp == NEXP + 1) {
         // ---------------------------------------------------------------- the pairs' lse
         for (Walk at = p.walk.at(blockIdx.x); ok && p.walk.in(at); p.walk.next(at)) {
-            if (!w.get(p, at, MK * MT)) continue;
+            if (!w.get(p, at)) continue;
             const int64_t flat0 = static_cast<int64_t>(w.b) * a.n_q * a.heads;
             for (int t = w.t0; t < w.t1; ++t, ++step) {
                 const uint32_t slot = step % NL;
@@ -332,21 +347,30 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
     } else {
         // ---------------------------------------------------------------- MMAs
         const int odd = warp - NEXP - 2;
-        uint32_t kn = 0;
+        Ring kr, qr;
         const uint32_t idesc = KV8 ? umma::idesc_e4m3(MK, p.n_cols) : umma::idesc_bf16(MK, p.n_cols, false, false);
         for (Walk at = p.walk.at(blockIdx.x); ok && p.walk.in(at); p.walk.next(at)) {
-            if (!w.get(p, at, MK * MT) || w.t0 == w.t1) continue;
+            if (!w.get(p, at) || w.t0 == w.t1) continue;
             const int t0 = uniform(w.t0), t1 = uniform(w.t1);
-            for (int t = t0; ok && t < t1; ++t, ++step) {
-                const uint32_t u = step & 1, qslot = step % QS;
+            for (int t = t0; ok && t < t1; ++t, ++step, qr.next(QS)) {
+                const uint32_t u = step & 1, qslot = qr.slot;
+                // this warp's 128-key tiles: slots of the ring
+                Ring kx[MT / 2];
+                kx[0] = kr;
+                if (odd) kx[0].next(KS);
+#pragma unroll
+                for (int i = 1; i < MT / 2; ++i) {
+                    kx[i] = kx[i - 1];
+                    kx[i].next(KS);
+                    kx[i].next(KS);
+                }
                 // lane 0: the pairs; 1, 2: S free; 3, 4: the keys
                 uint64_t* bar = lane == 0 ? &q_full[qslot] : nullptr;
-                uint32_t parity = (step / QS) & 1;
+                uint32_t parity = qr.phase;
 #pragma unroll
                 for (int i = 0; i < MT / 2; ++i) {
-                    const uint32_t kx = kn + 2 * i + odd;
                     if (lane == 1 + i && step >= 2) { bar = &s_empty[4 * u + 2 * i + odd]; parity = ((step >> 1) - 1) & 1; }
-                    if (lane == 3 + i && t == t0) { bar = &k_full[kx % KS]; parity = (kx / KS) & 1; }
+                    if (lane == 3 + i && t == t0) { bar = &k_full[kx[i].slot]; parity = kx[i].phase; }
                 }
                 if (!(ok = lanes_wait(bar, parity, &abort_flag, a.status))) break;
                 umma::fence_after();
@@ -354,7 +378,7 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
 #pragma unroll
                 for (int i = 0; i < MT / 2; ++i) {
                     const int mt = 2 * i + odd;
-                    const uint32_t s = (kn + mt) % KS;
+                    const uint32_t s = kx[i].slot;
                     const uint32_t kb = smem_u32(ks) + s * Sh::KTILE, d = tmem + 256 * u + mt * (256 / MT);
                     if (elect_one()) {
                         if (KV8) {
@@ -380,7 +404,8 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
                     __syncwarp();
                 }
             }
-            kn += MT;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) kr.next(KS);
         }
     }
     __syncwarp();
