@@ -116,6 +116,44 @@ struct Ring {
     }
 };
 
+// The weights of W columns of a key's lane added up: s the products, nl the pairs' -lse in log2
+// units (and, MK behind, their scales), c2 the key's factor.  WHOLE: all of them count; else
+// those in `see` (the others may hold anything).  Apart, and not a test per column: with the
+// branches in between nothing overlapped.
+template <bool KV8, bool WHOLE, bool POLY, int W>
+__device__ __forceinline__ void add_weights(const uint32_t (&s)[W], const float* nl, float2 c2, uint32_t see, float2& sum0,
+                                            float2& sum1) {
+#pragma unroll
+    for (int q = 0; q < W; q += 4) {
+        const float4 n4 = *reinterpret_cast<const float4*>(nl + q);
+        float2 ca = c2, cb = c2;
+        if (KV8) {
+            const float4 e4 = *reinterpret_cast<const float4*>(nl + MK + q);
+            const float2 z = make_float2(0.f, 0.f);
+            ca = fma2(c2, make_float2(e4.x, e4.y), z);
+            cb = fma2(c2, make_float2(e4.z, e4.w), z);
+        }
+        const float2 x0 = fma2(make_float2(__uint_as_float(s[q]), __uint_as_float(s[q + 1])), ca, make_float2(n4.x, n4.y));
+        const float2 x1 = fma2(make_float2(__uint_as_float(s[q + 2]), __uint_as_float(s[q + 3])), cb, make_float2(n4.z, n4.w));
+        float2 p0, p1;
+        if (POLY && ((kPolyGroups >> (q / 4)) & 1u)) {
+            p0 = exp2_poly2(x0);
+            p1 = exp2_poly2(x1);
+        } else {
+            p0 = make_float2(ex2(x0.x), ex2(x0.y));
+            p1 = make_float2(ex2(x1.x), ex2(x1.y));
+        }
+        if (!WHOLE) {
+            p0.x = (see >> q) & 1u ? p0.x : 0.f;
+            p0.y = (see >> (q + 1)) & 1u ? p0.y : 0.f;
+            p1.x = (see >> (q + 2)) & 1u ? p1.x : 0.f;
+            p1.y = (see >> (q + 3)) & 1u ? p1.y : 0.f;
+        }
+        sum0 = add2(sum0, p0);
+        sum1 = add2(sum1, p1);
+    }
+}
+
 template <int D, bool KV8, bool NARROW>
 __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant__ CUtensorMap kmap,
                                                           const __grid_constant__ CUtensorMap qmap,
@@ -163,46 +201,19 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
         // ---------------------------------------------------------------- exponentials
         const int quarter = warp & 3, mt = NARROW ? warp >> 2 : (warp >> 2) & 1, team = NARROW ? 0 : warp >> 3;
         const uint32_t ts = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + mt * (256 / MT);
-        constexpr int W = NARROW ? 16 : 32;
+        constexpr int W = NARROW ? 16 : 32, UN = NARROW ? 1 : 2;
         uint32_t it = 0;
         const float sc2 = a.scale * kLog2e;
-        // A thread's key in an item: the old total and the key's scale are loaded an item ahead.
-        struct Key {
-            int j, n;                                           // n: tiles of the item
-            bool closes, writes;                                // closes: the team of the last tile writes the totals
-            float old, ck;
-        };
-        auto key = [&](const Work<NARROW>& w, uint32_t step0) {
-            Key k;
-            k.j = w.j0 + MK * mt + 32 * quarter + lane;
-            k.n = w.t1 - w.t0;
-            k.closes = NARROW || (k.n == 0 ? team == 0 : static_cast<int>((step0 + k.n - 1) & 1) == team);
-            const bool live = k.j < w.end;
-            k.writes = k.closes && live;
-            const int64_t at = static_cast<int64_t>(w.b) * a.cap + k.j;
-            k.old = k.writes && a.splits == 1 && a.acc_in ? a.acc_in[at] : 0.f;
-            k.ck = KV8 && live ? __ldg(a.k_scale + at) : 1.f;
-            return k;
-        };
-        Walk pos = p.walk.at(blockIdx.x);
-        auto seek = [&](Work<NARROW>& w) {
-            for (; p.walk.in(pos); p.walk.next(pos))
-                if (w.get(p, pos)) return true;
-            return false;
-        };
-        bool more = seek(w);
-        Key k{};
-        if (more) k = key(w, 0);
-        while (ok && more) {
-            Work<NARROW> wn = w;
-            p.walk.next(pos);
-            more = seek(wn);
-            Key kx{};
-            if (more) kx = key(wn, step + k.n);
-            const int n = k.n, j = k.j;
-            const int64_t seq0 = static_cast<int64_t>(w.b) * a.cap;
-            const bool closes = k.closes, writes = k.writes;
-            const float ck = sc2 * k.ck, old = a.decay * k.old;
+        for (Walk at = p.walk.at(blockIdx.x); ok && p.walk.in(at); p.walk.next(at)) {
+            if (!w.get(p, at)) continue;
+            const int j = w.j0 + MK * mt + 32 * quarter + lane, n = w.t1 - w.t0;
+            const int64_t key = static_cast<int64_t>(w.b) * a.cap + j;
+            // the team of the last tile writes the totals
+            const bool closes = NARROW || (n == 0 ? team == 0 : static_cast<int>((step + n - 1) & 1) == team);
+            const bool writes = closes && j < w.end;
+            float old = 0.f, ck = sc2;
+            if (writes && a.splits == 1 && a.acc_in) old = a.acc_in[key];
+            if (KV8 && j < w.end) ck *= __ldg(a.k_scale + key);
             // this key is seen by the pairs from here on
             const int first = max(0, min(j, w.end - 1) - w.base) * a.heads;
             float total = 0.f;
@@ -217,7 +228,7 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
                 const int lo = first - t * p.n_cols;             // columns lo .. cols - 1 count
                 // a chunk of columns at a time, in a loop: with a tile's 64 or 128 columns unrolled the
                 // registers ran out and instructions came late
-#pragma unroll 1
+#pragma unroll UN
                 for (int c0 = 0; c0 < cols; c0 += W) {
                     uint32_t s[W];
                     tmem_ld(ts + 256 * u + c0, s);
@@ -231,35 +242,8 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&s_empty[4 * u + mt]);
                     }
-#pragma unroll
-                    for (int q = 0; q < W; q += 4) {
-                        const float4 n4 = *reinterpret_cast<const float4*>(nl + q);
-                        float2 ca = c2, cb = c2;
-                        if (KV8) {
-                            const float4 e4 = *reinterpret_cast<const float4*>(nl + MK + q);
-                            const float2 z = make_float2(0.f, 0.f);
-                            ca = fma2(c2, make_float2(e4.x, e4.y), z);
-                            cb = fma2(c2, make_float2(e4.z, e4.w), z);
-                        }
-                        const float2 x0 = fma2(make_float2(__uint_as_float(s[q]), __uint_as_float(s[q + 1])), ca, make_float2(n4.x, n4.y));
-                        const float2 x1 = fma2(make_float2(__uint_as_float(s[q + 2]), __uint_as_float(s[q + 3])), cb, make_float2(n4.z, n4.w));
-                        float2 p0, p1;
-                        if (!NARROW && ((kPolyGroups >> (q / 4)) & 1u)) {
-                            p0 = exp2_poly2(x0);
-                            p1 = exp2_poly2(x1);
-                        } else {
-                            p0 = make_float2(ex2(x0.x), ex2(x0.y));
-                            p1 = make_float2(ex2(x1.x), ex2(x1.y));
-                        }
-                        if (!whole) {                           // pairs that do not see the key, or hold anything
-                            if (!((see >> q) & 1u)) p0.x = 0.f;
-                            if (!((see >> (q + 1)) & 1u)) p0.y = 0.f;
-                            if (!((see >> (q + 2)) & 1u)) p1.x = 0.f;
-                            if (!((see >> (q + 3)) & 1u)) p1.y = 0.f;
-                        }
-                        sum0 = add2(sum0, p0);
-                        sum1 = add2(sum1, p1);
-                    }
+                    if (whole) add_weights<KV8, true, !NARROW, W>(s, nl, c2, see, sum0, sum1);
+                    else add_weights<KV8, false, false, W>(s, nl, c2, see, sum0, sum1);
                     total += (sum0.x + sum0.y) + (sum1.x + sum1.y);
                 }
                 __syncwarp();
@@ -282,11 +266,9 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
                 ++it;
             }
             if (writes) {
-                if (a.splits == 1) a.acc_out[seq0 + j] = old + total;
+                if (a.splits == 1) a.acc_out[key] = a.acc_in ? fmaf(a.decay, old, total) : total;
                 else a.part[(static_cast<int64_t>(w.split) * a.batch + w.b) * a.max_ctx + j] = total;
             }
-            w = wn;
-            k = kx;
         }
     } else if (warp == NEXP) {
         // ---------------------------------------------------------------- TMA loads
