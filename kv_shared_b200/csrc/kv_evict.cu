@@ -4,12 +4,15 @@
 // totals between them survive, in order.  Two launches:
 //
 //   select  one cluster of CTAs per sequence.  The totals' bit patterns, made to order like
-//           the values, are cut by three rounds of 11, 11 and 10 bits: each CTA counts its
-//           slice into shared memory, the cluster adds the counts, and the round's digit is
-//           the one in which the budget runs out.  The exact threshold pattern T and how
-//           many equal to it are still wanted (the lowest rows) follow; a last pass counts
-//           per warp and writes the survivors' rows in order, with no atomics on the output
-//           positions, so that equal calls give equal bits.
+//           the values, are counted by their upper 11 bits: each CTA counts its slice into
+//           shared memory, the cluster adds the counts, and the digit in which the budget
+//           runs out follows.  A second pass over the slice counts what lies above that digit
+//           and lists what has it (a few per cent of the rows); the lower 21 bits are then
+//           found from the lists alone, by rounds of 11 and 10 bits.  With the exact threshold
+//           pattern T and how many equal to it are still wanted (the lowest rows), a last pass
+//           writes the survivors' rows in order.  No atomic decides a position, so equal calls
+//           give equal bits.  A list that overflows (many equal totals) is not used: the later
+//           rounds then run over the slice.
 //   move    one warp per few rows copies K, V, scales and totals to their new places.
 //
 // Bound by HBM: 4 bytes per row of the totals (read once from HBM, then from L2) and twice
@@ -27,7 +30,11 @@ namespace {
 constexpr int ST = 1024;                         // threads of a select CTA
 constexpr int SW = ST / 32;
 constexpr int BINS = 2048;
-constexpr int LD = 8;                            // totals in flight per lane
+constexpr int COPIES = 4;                        // of the first round's counts (warps share them in turn)
+constexpr int kMaxCluster = 16;                  // more than 8 is an opt-in
+constexpr int LIST = 12288;                      // rows of a CTA's slice in the threshold's digit
+constexpr int LD = 16;                           // totals in flight per lane
+constexpr int kSelectSmem = (COPIES * BINS + BINS) * 4 + LIST * 8;
 
 // Bits that order like the values: -0 as 0, a NaN below everything.
 __device__ __forceinline__ uint32_t order_bits(float x) {
@@ -73,10 +80,14 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(EvictArgs a) {
     const int cs = static_cast<int>(cluster.num_blocks()), cr = static_cast<int>(cluster.block_rank());
     const int b = blockIdx.x / cs;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    __shared__ int hist[BINS], sums[BINS];
+    extern __shared__ int dyn[];
+    int* hist = dyn;                                            // [COPIES][BINS]
+    int* sums = hist + COPIES * BINS;                           // [BINS] over the cluster
+    uint2* list = reinterpret_cast<uint2*>(sums + BINS);        // [LIST] (pattern, row of the slice)
     __shared__ int scratch[SW + 1];
-    __shared__ int digit, rest, count2[2];
+    __shared__ int digit, rest, listed, count2[2];
     __shared__ int before2[2];
+    __shared__ int warp_gt[SW], warp_eq[SW];
 
     const int64_t keep = static_cast<int64_t>(a.sinks) + a.window + a.budget;
     int64_t n64 = a.len[b];
@@ -104,20 +115,71 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(EvictArgs a) {
 
     uint32_t prefix = 0;                                        // bits of T found so far
     int want = a.budget;                                        // still wanted among those that share them
+    int gt = 0;                                                 // of this lane, above the first digit
+    bool use_list = true;
+    if (tid < SW) warp_gt[tid] = warp_eq[tid] = 0;
+    if (tid == 0) listed = 0;
 #pragma unroll 1
     for (int round = 0; round < 3; ++round) {
         const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0);
         const uint32_t mask = round == 2 ? 1023u : 2047u;
         const uint32_t above = round == 0 ? 0u : (round == 1 ? 0xffe00000u : 0xfffffc00u);
-        for (int i = tid; i < BINS; i += ST) hist[i] = 0;
+        const int copies = round == 0 ? COPIES : 1;
+        for (int i = tid; i < copies * BINS; i += ST) hist[i] = 0;
         __syncthreads();
-        for (int i0 = s0; i0 < s1; i0 += 32 * LD) {
-            float x[LD];
-            load_part(acc, i0 + lane, s1, x);
+        if (round == 0) {
+            int* mine = hist + (warp % COPIES) * BINS;
+            for (int i0 = s0; i0 < s1; i0 += 32 * LD) {
+                float x[LD];
+                load_part(acc, i0 + lane, s1, x);
 #pragma unroll
-            for (int j = 0; j < LD; ++j) {
-                const uint32_t u = order_bits(x[j]);
-                if (i0 + 32 * j + lane < s1 && (u & above) == prefix) atomicAdd(&hist[(u >> shift) & mask], 1);
+                for (int j = 0; j < LD; ++j)
+                    if (i0 + 32 * j + lane < s1) atomicAdd(&mine[order_bits(x[j]) >> 21], 1);
+            }
+            __syncthreads();
+            for (int i = tid; i < BINS; i += ST) {
+                int c = hist[i];
+#pragma unroll
+                for (int k = 1; k < COPIES; ++k) c += hist[k * BINS + i];
+                hist[i] = c;
+            }
+        } else if (round == 1) {
+            // above the digit: counted; in it: listed, and counted by the next digit
+            for (int i0 = s0; i0 < s1; i0 += 32 * LD) {
+                float x[LD];
+                load_part(acc, i0 + lane, s1, x);
+#pragma unroll
+                for (int j = 0; j < LD; ++j) {
+                    const int i = i0 + 32 * j + lane;
+                    const uint32_t u = order_bits(x[j]);
+                    const bool in = i < s1, tie = in && (u & above) == prefix;
+                    gt += in && (u & above) > prefix;
+                    if (tie) atomicAdd(&hist[(u >> shift) & mask], 1);
+                    const uint32_t mt = __ballot_sync(0xffffffffu, tie);
+                    if (mt) {
+                        int at = 0;
+                        if (lane == 0) at = atomicAdd(&listed, __popc(mt));
+                        at = __shfl_sync(0xffffffffu, at, 0) + __popc(mt & ((1u << lane) - 1u));
+                        if (tie && at < LIST) list[at] = make_uint2(u, static_cast<uint32_t>(i - lo));
+                    }
+                }
+            }
+            __syncthreads();
+            use_list = listed <= LIST;                          // the same in every thread of the CTA
+        } else if (use_list) {
+            for (int i = tid; i < listed; i += ST) {
+                const uint32_t u = list[i].x;
+                if ((u & above) == prefix) atomicAdd(&hist[u & mask], 1);
+            }
+        } else {
+            for (int i0 = s0; i0 < s1; i0 += 32 * LD) {
+                float x[LD];
+                load_part(acc, i0 + lane, s1, x);
+#pragma unroll
+                for (int j = 0; j < LD; ++j) {
+                    const uint32_t u = order_bits(x[j]);
+                    if (i0 + 32 * j + lane < s1 && (u & above) == prefix) atomicAdd(&hist[u & mask], 1);
+                }
             }
         }
         cluster.sync();
@@ -142,17 +204,27 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(EvictArgs a) {
         want = rest;
         __syncthreads();
     }
-    // T = prefix; of the rows equal to it the first `want` are kept
-    int gt = 0, eq = 0;
-    for (int i0 = s0; i0 < s1; i0 += 32 * LD) {
-        float x[LD];
-        load_part(acc, i0 + lane, s1, x);
+    // T = prefix; of the rows equal to it the first `want` are kept.  Per warp: rows above T and
+    // equal to it.
+    int eq = 0;
+    if (use_list) {
+        for (int i = tid; i < listed; i += ST) {
+            const uint2 e = list[i];
+            if (e.x > prefix) atomicAdd(&warp_gt[e.y / seg], 1);
+            else if (e.x == prefix) atomicAdd(&warp_eq[e.y / seg], 1);
+        }
+    } else {
+        gt = 0;
+        for (int i0 = s0; i0 < s1; i0 += 32 * LD) {
+            float x[LD];
+            load_part(acc, i0 + lane, s1, x);
 #pragma unroll
-        for (int j = 0; j < LD; ++j) {
-            const bool in = i0 + 32 * j + lane < s1;
-            const uint32_t u = order_bits(x[j]);
-            gt += in && u > prefix;
-            eq += in && u == prefix;
+            for (int j = 0; j < LD; ++j) {
+                const bool in = i0 + 32 * j + lane < s1;
+                const uint32_t u = order_bits(x[j]);
+                gt += in && u > prefix;
+                eq += in && u == prefix;
+            }
         }
     }
 #pragma unroll
@@ -160,6 +232,9 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(EvictArgs a) {
         gt += __shfl_xor_sync(0xffffffffu, gt, o);
         eq += __shfl_xor_sync(0xffffffffu, eq, o);
     }
+    __syncthreads();
+    gt += warp_gt[warp];
+    eq += warp_eq[warp];
     int gt_all, eq_all;
     int gt_at = block_scan(lane == 0 ? gt : 0, scratch, &gt_all);
     int eq_at = block_scan(lane == 0 ? eq : 0, scratch, &eq_all);
@@ -250,20 +325,24 @@ void move(const EvictArgs& a, int64_t keep, cudaStream_t st) {
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
     const int64_t keep = static_cast<int64_t>(a.sinks) + a.window + a.budget;
-    // CTAs per sequence: as many as keep the batch on the SMs at once, up to the portable
-    // cluster size, and no more than leaves each a few thousand rows
+    // CTAs per sequence: as many as keep the batch on the SMs at once, up to the largest
+    // cluster, and no more than leaves each a few thousand rows
     int cs = 1;
-    while (cs < 8 && 2 * cs * a.batch <= num_sms() && a.cap > static_cast<int64_t>(cs) * 4096) cs *= 2;
+    while (cs < kMaxCluster && 2 * cs * a.batch <= num_sms() && a.cap > static_cast<int64_t>(cs) * 4096) cs *= 2;
+    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * cs);
     cfg.blockDim = dim3(ST);
+    cfg.dynamicSmemBytes = kSelectSmem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = cs; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
     if (e != cudaSuccess) return e;
     const int row = a.head_dim * (a.kv_dtype == HS2_F32 ? 4 : (a.kv_dtype == HS2_BF16 ? 2 : 1));
     if (row == 64) move<64>(a, keep, st);
