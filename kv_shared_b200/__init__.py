@@ -91,13 +91,16 @@ def lib():
     return _lib
 
 
+# Addresses go over as plain integers (the argument types make pointers of them): a call of
+# ten tensors spends less time here than its kernel runs.
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _check(fn, status):
