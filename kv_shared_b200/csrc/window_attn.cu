@@ -18,6 +18,7 @@
 // keys are cut over CTAs as well and a second launch joins the parts in a fixed order.
 #include "common.cuh"
 #include "internal.h"
+#include "tile_sync.cuh"
 #include "window_keys.cuh"
 
 namespace hs2 {
@@ -30,12 +31,6 @@ constexpr int F_ROWS = 64;                       // fp32: (row, head) pairs per 
 constexpr int F_KEYS = 32;                       // fp32: keys per tile
 constexpr int kMinSplitKeysF32 = 256;
 constexpr int64_t kTilePairs = 129;               // (row, head) pairs per sequence from which the tcgen05 kernel is taken
-
-// Four e4m3 codes -> two bf16 pairs, exact.
-__device__ __forceinline__ void codes_to_bf16(uint32_t v, uint32_t& lo, uint32_t& hi) {
-    lo = e4m3x2_to_bf16x2(static_cast<uint16_t>(v & 0xffffu));
-    hi = e4m3x2_to_bf16x2(static_cast<uint16_t>(v >> 16));
-}
 
 template <int D, bool KV8>
 struct Frag {
@@ -104,40 +99,66 @@ __device__ __forceinline__ int out_dim(int nt, int col, int t) {
 }
 
 template <int D, bool KV8>
-__global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a) {
+__global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a, FastDiv heads, FastDiv tiles) {
     using F = Frag<D, KV8>;
     constexpr int KS = D / 16;                   // k-steps of S
     constexpr int NT = D / 8;                    // n-tiles of O
-    extern __shared__ float sm[];                // [NW][16][D] O, then [NW][16] max, [NW][16] sum
+    constexpr int LDO = D + 4;                   // row pitch of the join
+    extern __shared__ float sm[];                // [NW][16][LDO] O, then [NW][16] max, [NW][16] sum
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int tiles = (a.n_q * a.heads + 15) / 16;
-    const int b = blockIdx.x / tiles, f0 = (blockIdx.x - b * tiles) * 16;
+    const int b = tiles.div(blockIdx.x), f0 = (blockIdx.x - b * static_cast<int>(tiles.d)) * 16;
     const int split = blockIdx.y;
     const int live = live_rows(a.n_rows, b, a.n_q);
     if (f0 >= live * a.heads) return;
     const int base = checked_base(a.q_pos0, b, live, a.max_ctx, a.status);
     const int f_last = min(f0 + 15, live * a.heads - 1);
-    const KeyList kl(base + f0 / a.heads, base + f_last / a.heads, a.window, a.sinks);
-    const int chunk = ((kl.total + a.splits - 1) / a.splits + STEP - 1) / STEP * STEP;
+    const KeyList kl(base + heads.div(f0), base + heads.div(f_last), a.window, a.sinks);
+    const int chunk = a.splits == 1 ? kl.total : ((kl.total + a.splits - 1) / a.splits + STEP - 1) / STEP * STEP;
     const int begin = min(kl.total, split * chunk), end = min(kl.total, begin + chunk);
     const int64_t seq0 = static_cast<int64_t>(b) * a.cap;
     const int64_t flat0 = static_cast<int64_t>(b) * a.n_q * a.heads;
 
+    F f;
+    int u0 = begin + warp * STEP;
+    if (u0 < end) {
+        load_k(f, a, seq0, kl, u0, end, g, t);
+        load_v(f, a, seq0, kl, u0, end, g, t);
+    }
     // Q fragments of pairs g and g + 8 in the keys' order of dims, and the pairs' positions
     uint32_t qa[KS][4];
     int pos[2];
+    float mag = 0.f;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        const int f = f0 + g + 8 * r;
-        pos[r] = f <= f_last ? base + f / a.heads : -1;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (flat0 + f) * D;
+        const int fr = f0 + g + 8 * r;
+        pos[r] = fr <= f_last ? base + heads.div(fr) : -1;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (flat0 + fr) * D;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             const int d = KV8 ? 16 * (t + 4 * (ks >> 2)) + 4 * (ks & 3) : 8 * (t + 4 * (ks >> 1)) + 4 * (ks & 1);
-            const uint2 x = f <= f_last ? __ldg(reinterpret_cast<const uint2*>(q + d)) : make_uint2(0, 0);
+            const uint2 x = fr <= f_last ? __ldg(reinterpret_cast<const uint2*>(q + d)) : make_uint2(0, 0);
             qa[ks][r] = x.x;
             qa[ks][2 + r] = x.y;
         }
+    }
+    float sc2 = a.scale * kLog2e;
+    if (KV8) {
+        // Q as f16 next to the codes' f16: times a power of two that brings its largest magnitude
+        // to [2^13, 2^14); what falls below f16's range then is 2^-38 of that
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mag = fmaxf(mag, fmaxf(fabsf(__uint_as_float(qa[ks][i] << 16)), fabsf(__uint_as_float(qa[ks][i] & 0xffff0000u))));
+        mag = warp_max(mag);
+        const int e = max(-120, min(120, 13 - (static_cast<int>(__float_as_uint(mag) >> 23) - 127)));
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                qa[ks][i] = pack_f16(__uint_as_float(qa[ks][i] << 16) * up, __uint_as_float(qa[ks][i] & 0xffff0000u) * up);
+        sc2 *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     }
 
     float o[NT][4];
@@ -146,16 +167,17 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    const float sc2 = a.scale * kLog2e;
 
-    F f;
-    int u0 = begin + warp * STEP;
-    if (u0 < end) {
-        load_k(f, a, seq0, kl, u0, end, g, t);
-        load_v(f, a, seq0, kl, u0, end, g, t);
-    }
     for (; u0 < end; u0 += NW * STEP) {
-        float s[2][4];
+        float s[2][4], lift[4];
+        if (KV8) {
+            // The value's scale belongs to its weight: weights are kept relative to the largest
+            // weight times scale, so that in f16 they are at most 1 and what f16 drops is 2^-25
+            // of that.
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lift[i] = fminf(fmaxf(__log2f(f.vs[i]), -60.f), 60.f);
+        }
+        float mn[2] = {m[0], m[1]};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -167,33 +189,35 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t b0, b1;
-                        codes_to_bf16(w[i], b0, b1);
-                        mma_bf16(s[h], qa[4 * c + i], b0, b1);
+                        e4m3x4_to_f16x2x2(w[i], b0, b1);
+                        mma_f16(s[h], qa[4 * c + i], b0, b1);
                     }
                 } else {
                     mma_bf16(s[h], qa[2 * c], w[0], w[1]);
                     mma_bf16(s[h], qa[2 * c + 1], w[2], w[3]);
                 }
             }
-            // logits in log2 units, hidden keys at -inf
+        }
+        const int un = u0 + NW * STEP;
+        float kf[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kf[i] = KV8 ? f.ks[i] * sc2 : sc2;
+        if (un < end) load_k(f, a, seq0, kl, un, end, g, t);
+        // logits in log2 units, hidden keys at -inf
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int u = u0 + 8 * h + 2 * t + (j & 1);
                 const int key = u < end ? kl.row(u) : -1;
-                const float x = KV8 ? s[h][j] * f.ks[2 * h + (j & 1)] * sc2 : s[h][j] * sc2;
-                s[h][j] = window_sees(key, pos[j >> 1], a.window, a.sinks) ? x : -INFINITY;
+                s[h][j] = window_sees(key, pos[j >> 1], a.window, a.sinks) ? s[h][j] * kf[2 * h + (j & 1)] : -INFINITY;
+                mn[j >> 1] = fmaxf(mn[j >> 1], KV8 ? s[h][j] + lift[2 * h + (j & 1)] : s[h][j]);
             }
-        }
-        const int un = u0 + NW * STEP;
-        if (un < end) load_k(f, a, seq0, kl, un, end, g, t);
-        float mn[2];
         bool rose = false;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            float x = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-            mn[r] = fmaxf(m[r], x);
+            mn[r] = fmaxf(mn[r], __shfl_xor_sync(0xffffffffu, mn[r], 1));
+            mn[r] = fmaxf(mn[r], __shfl_xor_sync(0xffffffffu, mn[r], 2));
             rose |= mn[r] > m[r];
         }
         if (__any_sync(0xffffffffu, rose)) {
@@ -215,31 +239,25 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const float off = m[r] == -INFINITY ? 0.f : m[r];
-                float p0 = ex2(s[h][2 * r] - off), p1 = ex2(s[h][2 * r + 1] - off);
+                const float p0 = ex2(s[h][2 * r] - off), p1 = ex2(s[h][2 * r + 1] - off);
                 l[r] += p0 + p1;
-                if (KV8) {
-                    p0 *= f.vs[2 * h];
-                    p1 *= f.vs[2 * h + 1];
-                }
-                // P in bf16: one rounding of at most 2^-8 relative per weight, the MMA's operand type
-                pa[2 * h + r] = pack_bf16(p0, p1);
+                // the MMA's operand type: a rounding of at most 2^-11 relative (f16), 2^-8 (bf16)
+                pa[2 * h + r] = KV8 ? pack_f16(p0 * f.vs[2 * h], p1 * f.vs[2 * h + 1]) : pack_bf16(p0, p1);
             }
-        if (KV8) {
-            // bytes of keys (2t, 2t + 1) side by side, then widened
 #pragma unroll
-            for (int w = 0; w < F::VW; ++w)
+        for (int w = 0; w < F::VW; ++w) {
+            if (KV8) {
+                // bytes of keys (2t, 2t + 1) side by side, then widened
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const uint32_t sel = q ? 0x7362u : 0x5140u;
                     uint32_t a0, a1, b0, b1;
-                    codes_to_bf16(prmt(f.v[0][w], f.v[1][w], sel), a0, a1);
-                    codes_to_bf16(prmt(f.v[2][w], f.v[3][w], sel), b0, b1);
-                    mma_bf16(o[(4 * w + 2 * q) % NT], pa, a0, b0);
-                    mma_bf16(o[(4 * w + 2 * q + 1) % NT], pa, a1, b1);
+                    e4m3x4_to_f16x2x2(prmt(f.v[0][w], f.v[1][w], sel), a0, a1);
+                    e4m3x4_to_f16x2x2(prmt(f.v[2][w], f.v[3][w], sel), b0, b1);
+                    mma_f16(o[(4 * w + 2 * q) % NT], pa, a0, b0);
+                    mma_f16(o[(4 * w + 2 * q + 1) % NT], pa, a1, b1);
                 }
-        } else {
-#pragma unroll
-            for (int w = 0; w < F::VW; ++w) {
+            } else {
                 mma_bf16(o[(2 * w) % NT], pa, prmt(f.v[0][w], f.v[1][w], 0x5410u), prmt(f.v[2][w], f.v[3][w], 0x5410u));
                 mma_bf16(o[(2 * w + 1) % NT], pa, prmt(f.v[0][w], f.v[1][w], 0x7632u),
                          prmt(f.v[2][w], f.v[3][w], 0x7632u));
@@ -248,10 +266,12 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a) {
         if (un < end) load_v(f, a, seq0, kl, un, end, g, t);
     }
 
-    // join the warps: pairs' maxima and sums, then O scaled to the common maximum
+    // join the warps: pairs' maxima and sums, then O scaled to the common maximum.  A thread's
+    // dims come in runs of four.
     float* so = sm;
-    float* s_m = sm + NW * 16 * D;
+    float* s_m = sm + NW * 16 * LDO;
     float* s_l = s_m + NW * 16;
+    const int active = min(NW, (end - begin + STEP - 1) / STEP);           // warps with keys
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -261,41 +281,54 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a) {
             s_l[warp * 16 + g + 8 * r] = l[r];
         }
     }
-    const int active = min(NW, (end - begin + STEP - 1) / STEP);           // warps with keys
     if (warp < active) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+        for (int i = 0; i < NT; i += 4)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                so[(warp * 16 + g + 8 * (j >> 1)) * D + out_dim<D, KV8>(i, j & 1, t)] = o[i][j];
+                *reinterpret_cast<float4*>(so + (warp * 16 + g + 8 * (j >> 1)) * LDO + out_dim<D, KV8>(i, j & 1, t)) =
+                    make_float4(o[i][j], o[i + 1][j], o[i + 2][j], o[i + 3][j]);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * D / 4; i += NW * 32) {
-        const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
-        if (f0 + r > f_last) continue;
-        float mx = -INFINITY;
-        for (int w = 0; w < active; ++w) mx = fmaxf(mx, s_m[w * 16 + r]);
-        float sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = 0; w < active; ++w) {
-            const float mw = s_m[w * 16 + r];
-            const float c = mw == -INFINITY ? 0.f : ex2(mw - mx);
-            const float4 x = *reinterpret_cast<const float4*>(so + (w * 16 + r) * D + d);
+    // NW * 32 / 16 threads to a pair, each with the same share of its dims
+    constexpr int TPP = NW * 2, PER = D / TPP;                             // 8 (4) dims
+    const int r = threadIdx.x / TPP, d = threadIdx.x % TPP * PER;
+    if (f0 + r > f_last) return;
+    float mw[NW], mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        mw[w] = w < active ? s_m[w * 16 + r] : -INFINITY;
+        mx = fmaxf(mx, mw[w]);
+    }
+    float sum = 0.f, acc[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+        if (mw[w] != -INFINITY) {
+            const float c = ex2(mw[w] - mx);
             sum = fmaf(c, s_l[w * 16 + r], sum);
-            acc.x = fmaf(c, x.x, acc.x); acc.y = fmaf(c, x.y, acc.y);
-            acc.z = fmaf(c, x.z, acc.z); acc.w = fmaf(c, x.w, acc.w);
+#pragma unroll
+            for (int i = 0; i < PER; i += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(so + (w * 16 + r) * LDO + d + i);
+                acc[i] = fmaf(c, x.x, acc[i]); acc[i + 1] = fmaf(c, x.y, acc[i + 1]);
+                acc[i + 2] = fmaf(c, x.z, acc[i + 2]); acc[i + 3] = fmaf(c, x.w, acc[i + 3]);
+            }
         }
-        const int64_t flat = flat0 + f0 + r;
-        if (a.splits == 1) {
-            const float inv = 1.f / sum;
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + flat * D + d) =
-                make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-            if (a.lse && d == 0) a.lse[flat] = (mx + log2f(sum)) * kLn2;
-        } else {
-            const int64_t at = static_cast<int64_t>(split) * a.batch * a.n_q * a.heads + flat;
-            *reinterpret_cast<float4*>(a.part_o + at * D + d) = acc;
-            if (d == 0) a.part_ml[at] = make_float2(mx, sum);
-        }
+    const int64_t flat = flat0 + f0 + r;
+    if (a.splits == 1) {
+        const float inv = 1.f / sum;
+#pragma unroll
+        for (int i = 0; i < PER; i += 4)
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + flat * D + d + i) =
+                make_uint2(pack_bf16(acc[i] * inv, acc[i + 1] * inv), pack_bf16(acc[i + 2] * inv, acc[i + 3] * inv));
+        if (a.lse && d == 0) a.lse[flat] = (mx + log2f(sum)) * kLn2;
+    } else {
+        const int64_t at = static_cast<int64_t>(split) * a.batch * a.n_q * a.heads + flat;
+#pragma unroll
+        for (int i = 0; i < PER; i += 4)
+            *reinterpret_cast<float4*>(a.part_o + at * D + d + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        if (d == 0) a.part_ml[at] = make_float2(mx, sum);
     }
 }
 
@@ -432,55 +465,62 @@ __global__ void __launch_bounds__(128) window_f32_kernel(WindowArgs a) {
     }
 }
 
-// Joins the parts of a pair: one warp per pair, D / 32 dims per lane, parts in order.
+// Joins the parts of a pair: D / 4 threads with four dims each and JOIN_Y of them to a pair,
+// which take the parts in turn; their sums are added in order.
+constexpr int JOIN_Y = 4;
 template <typename T, int D>
-__global__ void __launch_bounds__(128) window_join_kernel(WindowArgs a) {
-    constexpr int PER = D / 32;
+__global__ void __launch_bounds__(D / 4 * JOIN_Y) window_join_kernel(WindowArgs a, FastDiv rows) {
     const int64_t all = static_cast<int64_t>(a.batch) * a.n_q * a.heads;
-    const int64_t flat = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (flat >= all) return;
-    const int64_t row = flat / a.heads;
-    const int b = static_cast<int>(row / a.n_q);
-    if (row - static_cast<int64_t>(b) * a.n_q >= live_rows(a.n_rows, b, a.n_q)) return;
-    float mx = -INFINITY;
-    for (int s = lane; s < a.splits; s += 32) mx = fmaxf(mx, a.part_ml[s * all + flat].x);
-    mx = warp_max(mx);
-    float sum = 0.f, acc[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+    const int64_t flat = blockIdx.x;
+    const int b = rows.div(static_cast<int>(flat));              // rows.d: pairs per sequence
+    if (flat - static_cast<int64_t>(b) * rows.d >= static_cast<int64_t>(live_rows(a.n_rows, b, a.n_q)) * a.heads) return;
+    const int d = threadIdx.x * 4, y = threadIdx.y;
+    float mx = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
+    for (int s = y; s < a.splits; s += JOIN_Y) {
         const float2 ml = a.part_ml[s * all + flat];
-        float x[PER];
-        const float* src = a.part_o + (s * all + flat) * D + lane * PER;
-        if (PER == 4) {
-            const float4 y = *reinterpret_cast<const float4*>(src);
-            x[0] = y.x; x[1] = y.y; x[2 % PER] = y.z; x[3 % PER] = y.w;
-        } else {
-            const float2 y = *reinterpret_cast<const float2*>(src);
-            x[0] = y.x; x[1] = y.y;
-        }
-        const bool some = ml.x != -INFINITY;         // a part without keys may have left no O
-        const float c = some ? exp2f(ml.x - mx) : 0.f;
-        sum = fmaf(c, ml.y, sum);
+        const float4 x = *reinterpret_cast<const float4*>(a.part_o + (s * all + flat) * D + d);
+        if (ml.x == -INFINITY) continue;                         // a part without keys may have left no O
+        const float mn = fmaxf(mx, ml.x), c0 = exp2f(mx - mn), c1 = exp2f(ml.x - mn);
+        sum = fmaf(sum, c0, c1 * ml.y);
+        acc.x = fmaf(acc.x, c0, c1 * x.x); acc.y = fmaf(acc.y, c0, c1 * x.y);
+        acc.z = fmaf(acc.z, c0, c1 * x.z); acc.w = fmaf(acc.w, c0, c1 * x.w);
+        mx = mn;
+    }
+    __shared__ float4 s_o[JOIN_Y][D / 4];
+    __shared__ float2 s_ml[JOIN_Y];
+    s_o[y][threadIdx.x] = acc;
+    if (threadIdx.x == 0) s_ml[y] = make_float2(mx, sum);
+    __syncthreads();
+    if (y > 0) return;
+    mx = s_ml[0].x;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = fmaf(c, some ? x[i] : 0.f, acc[i]);
+    for (int i = 1; i < JOIN_Y; ++i) mx = fmaxf(mx, s_ml[i].x);
+    sum = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < JOIN_Y; ++i) {
+        const float c = s_ml[i].x == -INFINITY ? 0.f : exp2f(s_ml[i].x - mx);
+        const float4 x = s_o[i][threadIdx.x];
+        sum = fmaf(c, s_ml[i].y, sum);
+        acc.x = fmaf(c, x.x, acc.x); acc.y = fmaf(c, x.y, acc.y);
+        acc.z = fmaf(c, x.z, acc.z); acc.w = fmaf(c, x.w, acc.w);
     }
     const float inv = 1.f / sum;
-    T* dst = static_cast<T*>(a.o) + flat * D + lane * PER;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) dst[i] = static_cast<T>(acc[i] * inv);
-    if (a.lse && lane == 0) a.lse[flat] = (mx + log2f(sum)) * kLn2;
+    T* dst = static_cast<T*>(a.o) + flat * D + d;
+    dst[0] = static_cast<T>(acc.x * inv); dst[1] = static_cast<T>(acc.y * inv);
+    dst[2] = static_cast<T>(acc.z * inv); dst[3] = static_cast<T>(acc.w * inv);
+    if (a.lse && threadIdx.x == 0) a.lse[flat] = (mx + log2f(sum)) * kLn2;
 }
 
 template <int D, bool KV8>
 cudaError_t launch_rows(const WindowArgs& a, cudaStream_t st) {
-    constexpr int smem = (NW * 16 * D + 2 * NW * 16) * 4;
+    constexpr int smem = (NW * 16 * (D + 4) + 2 * NW * 16) * 4;
     const cudaError_t e = cudaFuncSetAttribute(window_rows_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const unsigned tiles = (static_cast<unsigned>(a.n_q) * a.heads + 15) / 16;
-    window_rows_kernel<D, KV8><<<dim3(tiles * a.batch, a.splits), NW * 32, smem, st>>>(a);
+    window_rows_kernel<D, KV8><<<dim3(tiles * a.batch, a.splits), NW * 32, smem, st>>>(a, FastDiv(a.heads), FastDiv(tiles));
     return cudaGetLastError();
 }
 
@@ -497,7 +537,7 @@ cudaError_t launch_f32(const WindowArgs& a, cudaStream_t st) {
 template <typename T, int D>
 cudaError_t launch_join(const WindowArgs& a, cudaStream_t st) {
     const int64_t all = static_cast<int64_t>(a.batch) * a.n_q * a.heads;
-    window_join_kernel<T, D><<<static_cast<unsigned>((all + 3) / 4), 128, 0, st>>>(a);
+    window_join_kernel<T, D><<<static_cast<unsigned>(all), dim3(D / 4, JOIN_Y), 0, st>>>(a, FastDiv(static_cast<uint32_t>(a.n_q) * a.heads));
     return cudaGetLastError();
 }
 
