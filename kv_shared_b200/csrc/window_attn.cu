@@ -6,16 +6,16 @@
 // the one K/V head, so (row, head) pairs are stacked: 16 consecutive pairs of a sequence
 // share every key that any of their rows attends to.
 //
-// Single tokens are bound by reading K and V once.  A warp takes 16 keys per step and keeps
-// the whole step in registers: keys and values come by 16-byte loads straight into the
-// fragments of m16n8k16 MMAs, no shared memory and no barrier in the loop.  For S = Q K^T
-// thread (g, t) of a warp holds chunks t, t + 4, .. of key g's row, which is a permutation of
-// the contraction index that Q's fragments follow; for O += P V it holds chunk g of keys 2t,
-// 2t + 1, 2t + 8, 2t + 9, whose dims become the MMA's n index (a permutation of the output
-// columns, undone on the way out).  The next step's keys are loaded as soon as S is formed
-// and its values as soon as they are used, so 4 to 8 KB per warp are always in flight.  The
-// warps' running (max, sum, O) are joined in shared memory; with few rows and many keys the
-// keys are cut over CTAs as well and a second launch joins the parts in a fixed order.
+// Single tokens are bound by reading K and V once.  Each warp takes steps of 16 keys from its
+// own ring of asynchronous copies in shared memory (no barrier but its own in the loop; with
+// one step ahead in registers a step took the memory's latency, 2.9 TB/s), and keeps the step
+// itself in registers.  For S = Q K^T thread (g, t) of a warp holds 16-byte chunks t, t + 4, ..
+// of key g's row, which is a permutation of the contraction index that Q's fragments follow;
+// for O += P V it holds chunk g of keys 2t, 2t + 1, 2t + 8, 2t + 9, whose dims become the MMA's
+// n index (a permutation of the output columns, undone on the way out).  Rows are stored with
+// their chunks shifted so that neither read meets a bank twice.  The warps' running (max, sum,
+// O) are joined in shared memory; with few rows and many keys the keys are cut over CTAs as
+// well and a second launch joins the parts in a fixed order.
 #include "common.cuh"
 #include "internal.h"
 #include "tile_sync.cuh"
@@ -38,57 +38,69 @@ struct Frag {
     static constexpr int KC = ROW / 64;                  // 16-byte K chunks per thread and 8 keys
     static constexpr int VB = ROW / 8;                   // V bytes per thread and key: 8, 16 or 32
     static constexpr int VW = VB / 4;                    // in 32-bit words
+    static constexpr int CPR = ROW / 16;                 // chunks of a row
+    static constexpr int PLANE = STEP * ROW;             // K or V of a step
+    static constexpr int STAGE = 2 * PLANE + (KV8 ? 2 * STEP * 4 : 0);      // K, V, their scales
+    // as many stages as shared memory has room for, up to 6
+    static constexpr int STAGES = 200 * 1024 / NW / STAGE < 6 ? 200 * 1024 / NW / STAGE : 6;
     uint4 k[2][KC];                                      // [8-key half][chunk]
     uint32_t v[4][VW];                                   // [key 2t, 2t+1, 2t+8, 2t+9][words]
     float ks[4], vs[4];                                  // scales of the same keys (e4m3)
-};
 
-template <int D, bool KV8>
-__device__ __forceinline__ void load_k(Frag<D, KV8>& f, const WindowArgs& a, int64_t seq0, const KeyList& kl, int u0,
-                                       int end, int g, int t) {
-    using F = Frag<D, KV8>;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int u = u0 + 8 * h + g;
-        const int key = u < end ? kl.row(u) : -1;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.k) + (seq0 + key) * F::ROW);
-#pragma unroll
-        for (int c = 0; c < F::KC; ++c)
-            f.k[h][c] = key >= 0 ? __ldg(src + t + 4 * c) : make_uint4(0, 0, 0, 0);
+    // where chunk c of row r lies in its plane: K is read by rows (neighbours' chunks t), V by
+    // every second row (one chunk)
+    static __device__ __forceinline__ int k_at(int r, int c) {
+        return r * ROW + ((CPR >= 8 ? (c & ~7) | ((c + 4 * (r & 1)) & 7) : c) << 4);
     }
-    if (KV8) {
+    static __device__ __forceinline__ int v_at(int r, int c) {
+        return r * ROW + ((CPR >= 8 ? (c & ~7) | ((c + 2 * ((r >> 1) & 3)) & 7) : (c + ((r >> 1) & 3)) & 3) << 4);
+    }
+    // the copies of keys u0 .. u0 + 15 of the list into a stage (whole warp); rows that hold no
+    // key become zeros
+    static __device__ __forceinline__ void copy(uint8_t* st, const WindowArgs& a, int64_t seq0, const KeyList& kl, int u0,
+                                                int end, int lane) {
+        constexpr int RPC = 32 / CPR < 1 ? 1 : 32 / CPR;         // rows per 32 chunks
+        const int c = lane % CPR;
+#pragma unroll
+        for (int r0 = 0; r0 < STEP; r0 += RPC) {
+            const int r = r0 + lane / CPR, u = u0 + r;
+            const int key = u < end ? kl.row(u) : -1;
+            const int64_t src = (seq0 + max(key, 0)) * ROW + c * 16;
+            cp_async16_zfill(st + k_at(r, c), static_cast<const uint8_t*>(a.k) + src, key >= 0);
+            cp_async16_zfill(st + PLANE + v_at(r, c), static_cast<const uint8_t*>(a.v) + src, key >= 0);
+        }
+        if (KV8) {
+            const int r = lane & 15, u = u0 + r;
+            const int key = u < end ? kl.row(u) : -1;
+            cp_async4_zfill(st + 2 * PLANE + lane * 4, (lane < 16 ? a.k_scale : a.v_scale) + seq0 + max(key, 0), key >= 0);
+        }
+    }
+    __device__ __forceinline__ void load(const uint8_t* st, int g, int t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < KC; ++c) k[h][c] = *reinterpret_cast<const uint4*>(st + k_at(8 * h + g, t + 4 * c));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int u = u0 + 8 * (i >> 1) + 2 * t + (i & 1);
-            const int key = u < end ? kl.row(u) : -1;
-            f.ks[i] = key >= 0 ? __ldg(a.k_scale + seq0 + key) : 0.f;
-        }
-    }
-}
-
-template <int D, bool KV8>
-__device__ __forceinline__ void load_v(Frag<D, KV8>& f, const WindowArgs& a, int64_t seq0, const KeyList& kl, int u0,
-                                       int end, int g, int t) {
-    using F = Frag<D, KV8>;
+            const int r = 8 * (i >> 1) + 2 * t + (i & 1);
+            if (VB == 8) {
+                const uint2 x = *reinterpret_cast<const uint2*>(st + PLANE + v_at(r, g >> 1) + 8 * (g & 1));
+                v[i][0] = x.x; v[i][1] = x.y;
+            } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int u = u0 + 8 * (i >> 1) + 2 * t + (i & 1);
-        const int key = u < end ? kl.row(u) : -1;
-        const uint8_t* src = static_cast<const uint8_t*>(a.v) + (seq0 + key) * F::ROW;
-        if (F::VB == 8) {
-            const uint2 x = key >= 0 ? __ldg(reinterpret_cast<const uint2*>(src) + g) : make_uint2(0, 0);
-            f.v[i][0] = x.x; f.v[i][1] = x.y;
-        } else {
-#pragma unroll
-            for (int c = 0; c < F::VB / 16; ++c) {
-                const uint4 x = key >= 0 ? __ldg(reinterpret_cast<const uint4*>(src) + g + 8 * c) : make_uint4(0, 0, 0, 0);
-                f.v[i][4 * c % F::VW] = x.x; f.v[i][(4 * c + 1) % F::VW] = x.y;
-                f.v[i][(4 * c + 2) % F::VW] = x.z; f.v[i][(4 * c + 3) % F::VW] = x.w;
+                for (int c = 0; c < VB / 16; ++c) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(st + PLANE + v_at(r, g + 8 * c));
+                    v[i][4 * c % VW] = x.x; v[i][(4 * c + 1) % VW] = x.y;
+                    v[i][(4 * c + 2) % VW] = x.z; v[i][(4 * c + 3) % VW] = x.w;
+                }
+            }
+            if (KV8) {
+                ks[i] = *reinterpret_cast<const float*>(st + 2 * PLANE + 4 * r);
+                vs[i] = *reinterpret_cast<const float*>(st + 2 * PLANE + 4 * (16 + r));
             }
         }
-        if (KV8) f.vs[i] = key >= 0 ? __ldg(a.v_scale + seq0 + key) : 0.f;
     }
-}
+};
 
 // First of the 16 consecutive output dims of thread t that n-tiles 8c .. 8c+7 hold: dims
 // +0..7 in the fragment's even column, +8..15 in the odd one (e4m3 rows of 128: 32 dims
@@ -104,7 +116,8 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a, F
     constexpr int KS = D / 16;                   // k-steps of S
     constexpr int NT = D / 8;                    // n-tiles of O
     constexpr int LDO = D + 4;                   // row pitch of the join
-    extern __shared__ float sm[];                // [NW][16][LDO] O, then [NW][16] max, [NW][16] sum
+    // the warps' rings; at the end [NW][16][LDO] O, then [NW][16] max, [NW][16] sum
+    extern __shared__ float sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int b = tiles.div(blockIdx.x), f0 = (blockIdx.x - b * static_cast<int>(tiles.d)) * 16;
     const int split = blockIdx.y;
@@ -118,11 +131,12 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a, F
     const int64_t seq0 = static_cast<int64_t>(b) * a.cap;
     const int64_t flat0 = static_cast<int64_t>(b) * a.n_q * a.heads;
 
-    F f;
+    uint8_t* ring = reinterpret_cast<uint8_t*>(sm) + warp * (F::STAGES * F::STAGE);
     int u0 = begin + warp * STEP;
-    if (u0 < end) {
-        load_k(f, a, seq0, kl, u0, end, g, t);
-        load_v(f, a, seq0, kl, u0, end, g, t);
+#pragma unroll
+    for (int i = 0; i < F::STAGES - 1; ++i) {
+        if (u0 + i * NW * STEP < end) F::copy(ring + i * F::STAGE, a, seq0, kl, u0 + i * NW * STEP, end, lane);
+        cp_async_commit();
     }
     // Q fragments of pairs g and g + 8 in the keys' order of dims, and the pairs' positions
     uint32_t qa[KS][4];
@@ -168,7 +182,18 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a, F
         for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-    for (; u0 < end; u0 += NW * STEP) {
+    for (int stage = 0; u0 < end; u0 += NW * STEP) {
+        const int un = u0 + (F::STAGES - 1) * NW * STEP;
+        int free = stage + F::STAGES - 1;                        // the stage read last
+        if (free >= F::STAGES) free -= F::STAGES;
+        if (un < end) F::copy(ring + free * F::STAGE, a, seq0, kl, un, end, lane);
+        cp_async_commit();
+        cp_async_wait<F::STAGES - 1>();
+        __syncwarp();
+        F f;
+        f.load(ring + stage * F::STAGE, g, t);
+        __syncwarp();                                            // before the next turn's copies into it
+        if (++stage == F::STAGES) stage = 0;
         float s[2][4], lift[4];
         if (KV8) {
             // The value's scale belongs to its weight: weights are kept relative to the largest
@@ -198,11 +223,9 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a, F
                 }
             }
         }
-        const int un = u0 + NW * STEP;
         float kf[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) kf[i] = KV8 ? f.ks[i] * sc2 : sc2;
-        if (un < end) load_k(f, a, seq0, kl, un, end, g, t);
         // logits in log2 units, hidden keys at -inf
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -263,11 +286,12 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a, F
                          prmt(f.v[2][w], f.v[3][w], 0x7632u));
             }
         }
-        if (un < end) load_v(f, a, seq0, kl, un, end, g, t);
     }
 
-    // join the warps: pairs' maxima and sums, then O scaled to the common maximum.  A thread's
-    // dims come in runs of four.
+    // join the warps: pairs' maxima and sums, then O scaled to the common maximum, in the rings'
+    // memory.  A thread's dims come in runs of four.
+    cp_async_wait<0>();
+    __syncthreads();
     float* so = sm;
     float* s_m = sm + NW * 16 * LDO;
     float* s_l = s_m + NW * 16;
@@ -516,7 +540,8 @@ __global__ void __launch_bounds__(D / 4 * JOIN_Y) window_join_kernel(WindowArgs 
 
 template <int D, bool KV8>
 cudaError_t launch_rows(const WindowArgs& a, cudaStream_t st) {
-    constexpr int smem = (NW * 16 * (D + 4) + 2 * NW * 16) * 4;
+    constexpr int join = (NW * 16 * (D + 4) + 2 * NW * 16) * 4, rings = NW * Frag<D, KV8>::STAGES * Frag<D, KV8>::STAGE;
+    constexpr int smem = join > rings ? join : rings;
     const cudaError_t e = cudaFuncSetAttribute(window_rows_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const unsigned tiles = (static_cast<unsigned>(a.n_q) * a.heads + 15) / 16;
