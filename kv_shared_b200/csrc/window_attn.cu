@@ -26,6 +26,7 @@ namespace {
 
 constexpr int NW = 8;                            // warps per CTA
 constexpr int STEP = 16;                         // keys per warp step
+constexpr float kLag = 4.f;                      // log2 units: weights stay below 2^4, f16's products far from its end
 constexpr int kMinSplitKeys = 512;               // keys per CTA below which a split costs more than it saves
 constexpr int F_ROWS = 64;                       // fp32: (row, head) pairs per CTA
 constexpr int F_KEYS = 32;                       // fp32: keys per tile
@@ -111,7 +112,7 @@ __device__ __forceinline__ int out_dim(int nt, int col, int t) {
 }
 
 template <int D, bool KV8>
-__global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a, FastDiv heads, FastDiv tiles) {
+__global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a, FastDiv heads, FastDiv tiles, FastDiv parts) {
     using F = Frag<D, KV8>;
     constexpr int KS = D / 16;                   // k-steps of S
     constexpr int NT = D / 8;                    // n-tiles of O
@@ -122,11 +123,12 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a, F
     const int b = tiles.div(blockIdx.x), f0 = (blockIdx.x - b * static_cast<int>(tiles.d)) * 16;
     const int split = blockIdx.y;
     const int live = live_rows(a.n_rows, b, a.n_q);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");         // the join may be set up; it waits for our end
     if (f0 >= live * a.heads) return;
     const int base = checked_base(a.q_pos0, b, live, a.max_ctx, a.status);
     const int f_last = min(f0 + 15, live * a.heads - 1);
     const KeyList kl(base + heads.div(f0), base + heads.div(f_last), a.window, a.sinks);
-    const int chunk = a.splits == 1 ? kl.total : ((kl.total + a.splits - 1) / a.splits + STEP - 1) / STEP * STEP;
+    const int chunk = a.splits == 1 ? kl.total : (parts.div(kl.total + a.splits - 1) + STEP - 1) / STEP * STEP;
     const int begin = min(kl.total, split * chunk), end = min(kl.total, begin + chunk);
     const int64_t seq0 = static_cast<int64_t>(b) * a.cap;
     const int64_t flat0 = static_cast<int64_t>(b) * a.n_q * a.heads;
@@ -181,6 +183,11 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a, F
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // list entries open_lo .. open_hi - 1 hold keys that all sixteen pairs see (where sinks lie
+    // inside the window's range, that range alone)
+    const int p_lo = base + heads.div(f0), p_hi = base + heads.div(f_last);
+    const int open_lo = f_last - f0 < 15 ? end : max(kl.s_pad, kl.s_pad + p_hi - a.window + 1 - kl.lo);
+    const int open_hi = min(end, kl.s_pad + p_lo - kl.lo + 1);
 
     for (int stage = 0; u0 < end; u0 += NW * STEP) {
         const int un = u0 + (F::STAGES - 1) * NW * STEP;
@@ -197,8 +204,8 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a, F
         float s[2][4], lift[4];
         if (KV8) {
             // The value's scale belongs to its weight: weights are kept relative to the largest
-            // weight times scale, so that in f16 they are at most 1 and what f16 drops is 2^-25
-            // of that.
+            // weight times scale, so that in f16 they are at most 2^kLag and what f16 drops is
+            // 2^-25 of it.
 #pragma unroll
             for (int i = 0; i < 4; ++i) lift[i] = fminf(fmaxf(__log2f(f.vs[i]), -60.f), 60.f);
         }
@@ -226,27 +233,40 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a, F
         float kf[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) kf[i] = KV8 ? f.ks[i] * sc2 : sc2;
-        // logits in log2 units, hidden keys at -inf
+        // logits in log2 units, hidden keys at -inf; most steps hide none
+        const bool whole = u0 >= open_lo && u0 + STEP <= open_hi;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int u = u0 + 8 * h + 2 * t + (j & 1);
-                const int key = u < end ? kl.row(u) : -1;
-                s[h][j] = window_sees(key, pos[j >> 1], a.window, a.sinks) ? s[h][j] * kf[2 * h + (j & 1)] : -INFINITY;
+            for (int j = 0; j < 4; ++j) s[h][j] *= kf[2 * h + (j & 1)];
+        if (!whole) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int u = u0 + 8 * h + 2 * t + (j & 1);
+                    const int key = u < end ? kl.row(u) : -1;
+                    if (!window_sees(key, pos[j >> 1], a.window, a.sinks)) s[h][j] = -INFINITY;
+                }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
                 mn[j >> 1] = fmaxf(mn[j >> 1], KV8 ? s[h][j] + lift[2 * h + (j & 1)] : s[h][j]);
-            }
+        // the reference may trail the maximum by kLag: O is rescaled now and then, not every step
         bool rose = false;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             mn[r] = fmaxf(mn[r], __shfl_xor_sync(0xffffffffu, mn[r], 1));
             mn[r] = fmaxf(mn[r], __shfl_xor_sync(0xffffffffu, mn[r], 2));
+            if (!(mn[r] > m[r] + kLag)) mn[r] = m[r] == -INFINITY ? mn[r] : m[r];
             rose |= mn[r] > m[r];
         }
         if (__any_sync(0xffffffffu, rose)) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const float c = mn[r] == -INFINITY ? 1.f : ex2(m[r] - mn[r]);
+                const float c = m[r] == -INFINITY ? 1.f : ex2(m[r] - mn[r]);       // from -inf: l and O are zero
                 l[r] *= c;
                 m[r] = mn[r];
 #pragma unroll
@@ -491,7 +511,7 @@ __global__ void __launch_bounds__(128) window_f32_kernel(WindowArgs a) {
 
 // Joins the parts of a pair: D / 4 threads with four dims each and JOIN_Y of them to a pair,
 // which take the parts in turn; their sums are added in order.
-constexpr int JOIN_Y = 4;
+constexpr int JOIN_Y = 8;
 template <typename T, int D>
 __global__ void __launch_bounds__(D / 4 * JOIN_Y) window_join_kernel(WindowArgs a, FastDiv rows) {
     const int64_t all = static_cast<int64_t>(a.batch) * a.n_q * a.heads;
@@ -501,16 +521,26 @@ __global__ void __launch_bounds__(D / 4 * JOIN_Y) window_join_kernel(WindowArgs 
     const int d = threadIdx.x * 4, y = threadIdx.y;
     float mx = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = y; s < a.splits; s += JOIN_Y) {
-        const float2 ml = a.part_ml[s * all + flat];
-        const float4 x = *reinterpret_cast<const float4*>(a.part_o + (s * all + flat) * D + d);
-        if (ml.x == -INFINITY) continue;                         // a part without keys may have left no O
-        const float mn = fmaxf(mx, ml.x), c0 = exp2f(mx - mn), c1 = exp2f(ml.x - mn);
-        sum = fmaf(sum, c0, c1 * ml.y);
-        acc.x = fmaf(acc.x, c0, c1 * x.x); acc.y = fmaf(acc.y, c0, c1 * x.y);
-        acc.z = fmaf(acc.z, c0, c1 * x.z); acc.w = fmaf(acc.w, c0, c1 * x.w);
-        mx = mn;
+    asm volatile("griddepcontrol.wait;" ::: "memory");          // launched early: the parts are there from here on
+    constexpr int AHEAD = 5;                                     // parts in flight per thread
+    for (int s0 = y; s0 < a.splits; s0 += JOIN_Y * AHEAD) {
+        float2 ml[AHEAD];
+        float4 x[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int s = s0 + i * JOIN_Y;
+            ml[i] = s < a.splits ? a.part_ml[s * all + flat] : make_float2(-INFINITY, 0.f);
+            x[i] = s < a.splits ? *reinterpret_cast<const float4*>(a.part_o + (s * all + flat) * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (ml[i].x == -INFINITY) continue;                  // a part without keys may have left no O
+            const float mn = fmaxf(mx, ml[i].x), c0 = exp2f(mx - mn), c1 = exp2f(ml[i].x - mn);
+            sum = fmaf(sum, c0, c1 * ml[i].y);
+            acc.x = fmaf(acc.x, c0, c1 * x[i].x); acc.y = fmaf(acc.y, c0, c1 * x[i].y);
+            acc.z = fmaf(acc.z, c0, c1 * x[i].z); acc.w = fmaf(acc.w, c0, c1 * x[i].w);
+            mx = mn;
+        }
     }
     __shared__ float4 s_o[JOIN_Y][D / 4];
     __shared__ float2 s_ml[JOIN_Y];
@@ -545,7 +575,7 @@ cudaError_t launch_rows(const WindowArgs& a, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(window_rows_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const unsigned tiles = (static_cast<unsigned>(a.n_q) * a.heads + 15) / 16;
-    window_rows_kernel<D, KV8><<<dim3(tiles * a.batch, a.splits), NW * 32, smem, st>>>(a, FastDiv(a.heads), FastDiv(tiles));
+    window_rows_kernel<D, KV8><<<dim3(tiles * a.batch, a.splits), NW * 32, smem, st>>>(a, FastDiv(a.heads), FastDiv(tiles), FastDiv(a.splits));
     return cudaGetLastError();
 }
 
@@ -562,8 +592,16 @@ cudaError_t launch_f32(const WindowArgs& a, cudaStream_t st) {
 template <typename T, int D>
 cudaError_t launch_join(const WindowArgs& a, cudaStream_t st) {
     const int64_t all = static_cast<int64_t>(a.batch) * a.n_q * a.heads;
-    window_join_kernel<T, D><<<static_cast<unsigned>(all), dim3(D / 4, JOIN_Y), 0, st>>>(a, FastDiv(static_cast<uint32_t>(a.n_q) * a.heads));
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(all));
+    cfg.blockDim = dim3(D / 4, JOIN_Y);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, window_join_kernel<T, D>, a, FastDiv(static_cast<uint32_t>(a.n_q) * a.heads));
 }
 
 }  // namespace
