@@ -28,8 +28,9 @@ constexpr int NW = 8;                            // warps per CTA
 constexpr int STEP = 16;                         // keys per warp step
 constexpr float kLag = 4.f;                      // log2 units: weights stay below 2^4, f16's products far from its end
 constexpr int kMinSplitKeys = 512;               // keys per CTA below which a split costs more than it saves
-constexpr int F_ROWS = 64;                       // fp32: (row, head) pairs per CTA
-constexpr int F_KEYS = 32;                       // fp32: keys per tile
+constexpr int F_QT = 8;                          // fp32: threads that share two pairs
+constexpr int F_ROWS = 2 * 128 / F_QT;           // (row, head) pairs per CTA
+constexpr int F_KEYS = 32;                       // keys per tile
 constexpr int kMinSplitKeysF32 = 256;
 constexpr int64_t kTilePairs = 129;               // (row, head) pairs per sequence from which the tcgen05 kernel is taken
 
@@ -376,19 +377,20 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a, F
     }
 }
 
-// fp32: 64 pairs x 32 keys per tile on the CUDA cores (a bf16 or tf32 product would lose
-// what the fp32 caches are there for).  Thread (rp, qt) of 32 x 4 has pairs 2 rp, 2 rp + 1;
-// keys qt + 4 i of S, dims 4 qt + 16 i of O: nine or ten 16-byte shared loads per 64 FMAs.
+// fp32: 32 pairs x 32 keys per tile on the CUDA cores (a bf16 or tf32 product would lose what
+// the fp32 caches are there for).  Thread (rp, qt) of 16 x 8 has pairs 2 rp, 2 rp + 1; keys
+// qt + 8 i of S, dims 4 (qt + 8 j) of O.
 template <int D>
 __global__ void __launch_bounds__(128) window_f32_kernel(WindowArgs a) {
     constexpr int LDQ = D + 4;                   // row pitch: rows of a quarter-warp on distinct banks
-    constexpr int NC = D / 16;                   // float4 chunks of O per thread and pair
+    constexpr int LDP = F_KEYS + 4;
+    constexpr int NC = D / (4 * F_QT);           // float4 chunks of O per thread and pair
+    constexpr int KPT = F_KEYS / F_QT;           // keys of S per thread and pair
     extern __shared__ float4 sm4[];
-    float* sq = reinterpret_cast<float*>(sm4);   // [64][LDQ]
-    float* sk = sq + F_ROWS * LDQ;               // [32][LDQ]
-    float* sv = sk + F_KEYS * LDQ;               // [32][D]
-    float* sp = sv + F_KEYS * D;                 // [64][33]
-    const int tid = threadIdx.x, rp = tid >> 2, qt = tid & 3;
+    float* sq = reinterpret_cast<float*>(sm4);   // [F_ROWS][LDQ]
+    float* sp = sq + F_ROWS * LDQ;               // [F_ROWS][LDP]
+    float* kv = sp + F_ROWS * LDP;               // [2] K [F_KEYS][LDQ], V [F_KEYS][D]: a tile ahead
+    const int tid = threadIdx.x, rp = tid / F_QT, qt = tid % F_QT;
     const int tiles = (a.n_q * a.heads + F_ROWS - 1) / F_ROWS;
     const int b = blockIdx.x / tiles, f0 = (blockIdx.x - b * tiles) * F_ROWS;
     const int live = live_rows(a.n_rows, b, a.n_q);
@@ -418,32 +420,40 @@ __global__ void __launch_bounds__(128) window_f32_kernel(WindowArgs a) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int u0 = begin; u0 < end; u0 += F_KEYS) {
-        __syncthreads();
+    auto copy = [&](int u0, int buf) {
+        float* sk = kv + buf * F_KEYS * (LDQ + D);
+        float* sv = sk + F_KEYS * LDQ;
+#pragma unroll
         for (int i = tid; i < F_KEYS * D / 4; i += 128) {
             const int r = i / (D / 4), c = i - r * (D / 4);
             const int key = u0 + r < end ? kl.row(u0 + r) : -1;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-            if (key >= 0) {
-                x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.k) + (seq0 + key) * D) + c);
-                y = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.v) + (seq0 + key) * D) + c);
-            }
-            *reinterpret_cast<float4*>(sk + r * LDQ + 4 * c) = x;
-            *reinterpret_cast<float4*>(sv + r * D + 4 * c) = y;
+            const int64_t src = (seq0 + max(key, 0)) * D + 4 * c;
+            cp_async16_zfill(sk + r * LDQ + 4 * c, static_cast<const float*>(a.k) + src, key >= 0);
+            cp_async16_zfill(sv + r * D + 4 * c, static_cast<const float*>(a.v) + src, key >= 0);
         }
+    };
+    if (begin < end) copy(begin, 0);
+    cp_async_commit();
+    int buf = 0;
+    for (int u0 = begin; u0 < end; u0 += F_KEYS, buf ^= 1) {
+        if (u0 + F_KEYS < end) copy(u0 + F_KEYS, buf ^ 1);
+        cp_async_commit();
+        cp_async_wait<1>();
         __syncthreads();
-        float s[2][8];
+        const float* sk = kv + buf * F_KEYS * (LDQ + D);
+        const float* sv = sk + F_KEYS * LDQ;
+        float s[2][KPT];
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[r][i] = 0.f;
-#pragma unroll 4
+            for (int i = 0; i < KPT; ++i) s[r][i] = 0.f;
+#pragma unroll 8
         for (int c = 0; c < D / 4; ++c) {
             const float4 x0 = *reinterpret_cast<const float4*>(sq + (2 * rp) * LDQ + 4 * c);
             const float4 x1 = *reinterpret_cast<const float4*>(sq + (2 * rp + 1) * LDQ + 4 * c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float4 y = *reinterpret_cast<const float4*>(sk + (qt + 4 * i) * LDQ + 4 * c);
+            for (int i = 0; i < KPT; ++i) {
+                const float4 y = *reinterpret_cast<const float4*>(sk + (qt + F_QT * i) * LDQ + 4 * c);
                 s[0][i] = fmaf(x0.x, y.x, fmaf(x0.y, y.y, fmaf(x0.z, y.z, fmaf(x0.w, y.w, s[0][i]))));
                 s[1][i] = fmaf(x1.x, y.x, fmaf(x1.y, y.y, fmaf(x1.z, y.z, fmaf(x1.w, y.w, s[1][i]))));
             }
@@ -452,46 +462,51 @@ __global__ void __launch_bounds__(128) window_f32_kernel(WindowArgs a) {
         for (int r = 0; r < 2; ++r) {
             float mx = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int u = u0 + qt + 4 * i;
+            for (int i = 0; i < KPT; ++i) {
+                const int u = u0 + qt + F_QT * i;
                 const int key = u < end ? kl.row(u) : -1;
                 s[r][i] = window_sees(key, pos[r], a.window, a.sinks) ? s[r][i] * sc2 : -INFINITY;
                 mx = fmaxf(mx, s[r][i]);
             }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+#pragma unroll
+            for (int o1 = 1; o1 < F_QT; o1 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o1));
             const float mn = fmaxf(m[r], mx);
             const float c = mn == -INFINITY ? 1.f : exp2f(m[r] - mn), off = mn == -INFINITY ? 0.f : mn;
             float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < KPT; ++i) {
                 const float p = exp2f(s[r][i] - off);
                 sum += p;
-                sp[(2 * rp + r) * 33 + qt + 4 * i] = p;
+                sp[(2 * rp + r) * LDP + qt + F_QT * i] = p;
             }
             l[r] = fmaf(l[r], c, sum);
             m[r] = mn;
 #pragma unroll
             for (int j = 0; j < NC; ++j) { o[r][j].x *= c; o[r][j].y *= c; o[r][j].z *= c; o[r][j].w *= c; }
         }
-        __syncwarp();                            // a pair's weights come from the four threads of its quad
+        __syncwarp();                            // a pair's weights come from its F_QT neighbouring threads
 #pragma unroll 4
-        for (int k = 0; k < F_KEYS; ++k) {
-            const float p0 = sp[(2 * rp) * 33 + k], p1 = sp[(2 * rp + 1) * 33 + k];
+        for (int k = 0; k < F_KEYS; k += 4) {
+            const float4 w0 = *reinterpret_cast<const float4*>(sp + (2 * rp) * LDP + k);
+            const float4 w1 = *reinterpret_cast<const float4*>(sp + (2 * rp + 1) * LDP + k);
+            const float p0[4] = {w0.x, w0.y, w0.z, w0.w}, p1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-            for (int j = 0; j < NC; ++j) {
-                const float4 y = *reinterpret_cast<const float4*>(sv + k * D + 4 * qt + 16 * j);
-                o[0][j].x = fmaf(p0, y.x, o[0][j].x); o[0][j].y = fmaf(p0, y.y, o[0][j].y);
-                o[0][j].z = fmaf(p0, y.z, o[0][j].z); o[0][j].w = fmaf(p0, y.w, o[0][j].w);
-                o[1][j].x = fmaf(p1, y.x, o[1][j].x); o[1][j].y = fmaf(p1, y.y, o[1][j].y);
-                o[1][j].z = fmaf(p1, y.z, o[1][j].z); o[1][j].w = fmaf(p1, y.w, o[1][j].w);
-            }
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < NC; ++j) {
+                    const float4 y = *reinterpret_cast<const float4*>(sv + (k + i) * D + 4 * (qt + F_QT * j));
+                    o[0][j].x = fmaf(p0[i], y.x, o[0][j].x); o[0][j].y = fmaf(p0[i], y.y, o[0][j].y);
+                    o[0][j].z = fmaf(p0[i], y.z, o[0][j].z); o[0][j].w = fmaf(p0[i], y.w, o[0][j].w);
+                    o[1][j].x = fmaf(p1[i], y.x, o[1][j].x); o[1][j].y = fmaf(p1[i], y.y, o[1][j].y);
+                    o[1][j].z = fmaf(p1[i], y.z, o[1][j].z); o[1][j].w = fmaf(p1[i], y.w, o[1][j].w);
+                }
         }
+        __syncthreads();                         // the tile may be overwritten
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+#pragma unroll
+        for (int o1 = 1; o1 < F_QT; o1 <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o1);
         const int f = f0 + 2 * rp + r;
         if (f > f_last) continue;
         const int64_t flat = flat0 + f;
@@ -500,7 +515,7 @@ __global__ void __launch_bounds__(128) window_f32_kernel(WindowArgs a) {
         float* dst = a.splits == 1 ? static_cast<float*>(a.o) + flat * D : a.part_o + at * D;
 #pragma unroll
         for (int j = 0; j < NC; ++j)
-            *reinterpret_cast<float4*>(dst + 4 * qt + 16 * j) =
+            *reinterpret_cast<float4*>(dst + 4 * (qt + F_QT * j)) =
                 make_float4(o[r][j].x * inv, o[r][j].y * inv, o[r][j].z * inv, o[r][j].w * inv);
         if (qt == 0) {
             if (a.splits > 1) a.part_ml[at] = make_float2(m[r], l[r]);
@@ -581,7 +596,7 @@ cudaError_t launch_rows(const WindowArgs& a, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_f32(const WindowArgs& a, cudaStream_t st) {
-    constexpr int smem = ((F_ROWS + F_KEYS) * (D + 4) + F_KEYS * D + F_ROWS * 33) * 4;
+    constexpr int smem = (F_ROWS * (D + 4) + F_ROWS * (F_KEYS + 4) + 2 * F_KEYS * (2 * D + 4)) * 4;
     const cudaError_t e = cudaFuncSetAttribute(window_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const unsigned tiles = (static_cast<unsigned>(a.n_q) * a.heads + F_ROWS - 1) / F_ROWS;
