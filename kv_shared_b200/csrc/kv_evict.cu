@@ -13,6 +13,9 @@
 //           writes the survivors' rows in order.  No atomic decides a position, so equal calls
 //           give equal bits.  A list that overflows (many equal totals) is not used: the later
 //           rounds then run over the slice.
+//           Where clusters would leave SMs idle, the same is done by a team of SMs / batch CTAs per sequence that meet in grid-wide barriers (a
+//           cooperative launch) and hold their slices' patterns in shared memory; their counts
+//           meet in the sequence's rows of k_out, which the move then overwrites.
 //   move    one warp per few rows copies K, V, scales and totals to their new places.
 //
 // Bound by HBM: 4 bytes per row of the totals (read once from HBM, then from L2) and twice
@@ -266,6 +269,144 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(EvictArgs a) {
     }
 }
 
+// The same by a team of `team` CTAs per sequence, slices in shared memory.
+constexpr int kKeys = 40960;                     // rows of a CTA's slice, at most
+constexpr int kGridSmem = (COPIES * BINS + kKeys) * 4;
+constexpr int kScratchInts = 3 * BINS;           // counts of the three rounds; then two per CTA
+
+__global__ void __launch_bounds__(ST) evict_grid_kernel(EvictArgs a, int team, int row_bytes) {
+    cg::grid_group grid = cg::this_grid();
+    const int b = blockIdx.x / team, tr = blockIdx.x - b * team;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    extern __shared__ int dyn[];
+    int* hist = dyn;                                            // [COPIES][BINS]
+    uint32_t* keys = reinterpret_cast<uint32_t*>(hist + COPIES * BINS);   // [kKeys]
+    __shared__ int scratch[SW + 1];
+    __shared__ int digit, rest, before2[2];
+
+    const int64_t keep = static_cast<int64_t>(a.sinks) + a.window + a.budget;
+    int64_t n64 = a.len[b];
+    n64 = n64 < 0 ? 0 : (n64 > a.cap ? a.cap : n64);
+    const int n = static_cast<int>(n64);
+    const int kept = n < keep ? n : static_cast<int>(keep);
+    int32_t* idx = a.idx + b * keep;
+    if (tr == 0 && tid == 0) a.new_len[b] = kept;
+    for (int64_t i = kept + tr * ST + tid; i < keep; i += team * ST) idx[i] = -1;
+    const bool cut = n > keep && a.budget > 0;                  // the same in the whole team
+    const int first = a.sinks, m = cut ? n - a.window - a.sinks : 0;
+    if (n <= keep) {
+        for (int i = tr * ST + tid; i < n; i += team * ST) idx[i] = i;
+    } else {
+        for (int i = tr * ST + tid; i < a.sinks; i += team * ST) idx[i] = i;
+        for (int i = tr * ST + tid; i < a.window; i += team * ST) idx[a.sinks + a.budget + i] = n - a.window + i;
+    }
+    const int per = (m + team - 1) / team;
+    const int lo = min(m, tr * per), mine = min(m, lo + per) - lo;
+    const float* acc = a.acc + b * a.cap + first + lo;
+    // the sequence's rows of k_out: only where rows are cut, hence all of them written later
+    int* counts = reinterpret_cast<int*>(static_cast<uint8_t*>(a.k_out) + static_cast<int64_t>(b) * a.out_cap * row_bytes);
+    for (int i = tid; i < COPIES * BINS; i += ST) hist[i] = 0;
+    if (cut)
+        for (int i = tr * ST + tid; i < kScratchInts; i += team * ST) counts[i] = 0;
+    __syncthreads();
+    int* copy = hist + (warp % COPIES) * BINS;
+    for (int i0 = 0; i0 < mine; i0 += ST * 8) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = i0 + j * ST + tid < mine ? __ldg(acc + i0 + j * ST + tid) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (i0 + j * ST + tid < mine) {
+                const uint32_t u = order_bits(x[j]);
+                keys[i0 + j * ST + tid] = u;
+                atomicAdd(&copy[u >> 21], 1);
+            }
+    }
+    __syncthreads();
+    grid.sync();                                                // the counts are zero
+    uint32_t prefix = 0;                                        // bits of T found so far
+    int want = a.budget;
+#pragma unroll 1
+    for (int round = 0; round < 3; ++round) {
+        const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0);
+        const uint32_t mask = round == 2 ? 1023u : 2047u;
+        const uint32_t above = round == 0 ? 0u : (round == 1 ? 0xffe00000u : 0xfffffc00u);
+        if (round > 0) {
+            for (int i = tid; i < BINS; i += ST) hist[i] = 0;
+            __syncthreads();
+            for (int i = tid; i < mine; i += ST) {
+                const uint32_t u = keys[i];
+                if ((u & above) == prefix) atomicAdd(&hist[(u >> shift) & mask], 1);
+            }
+            __syncthreads();
+        }
+        if (cut)
+            for (int i = tid; i < BINS; i += ST) {
+                int c = hist[i];
+                if (round == 0)
+#pragma unroll
+                    for (int k = 1; k < COPIES; ++k) c += hist[k * BINS + i];
+                if (c) atomicAdd(&counts[round * BINS + i], c);
+            }
+        grid.sync();
+        if (cut) {
+            // the digit in which the budget runs out: thread t has the bins 2047 - 2t and 2046 - 2t
+            const int2 c = __ldcg(reinterpret_cast<const int2*>(counts + round * BINS) + (BINS / 2 - 1 - tid));
+            int total;
+            const int over = block_scan(c.x + c.y, scratch, &total);
+            if (over < want && over + c.y >= want) { digit = BINS - 1 - 2 * tid; rest = want - over; }
+            else if (over + c.y < want && over + c.y + c.x >= want) { digit = BINS - 2 - 2 * tid; rest = want - over - c.y; }
+            __syncthreads();
+            prefix |= static_cast<uint32_t>(digit) << shift;
+            want = rest;
+            __syncthreads();
+        }
+    }
+    // rows above T = prefix and equal to it: of this warp's part of the slice, of the CTA, of the
+    // CTAs before
+    const int seg = ((mine + SW - 1) / SW + 31) & ~31;          // whole warps wide
+    const int s0 = min(mine, warp * seg), s1 = min(mine, s0 + seg);
+    int gt = 0, eq = 0;
+    for (int i = s0 + lane; i < s1; i += 32) {
+        const uint32_t u = keys[i];
+        gt += u > prefix;
+        eq += u == prefix;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        gt += __shfl_xor_sync(0xffffffffu, gt, o);
+        eq += __shfl_xor_sync(0xffffffffu, eq, o);
+    }
+    int gt_all, eq_all;
+    int gt_at = block_scan(lane == 0 ? gt : 0, scratch, &gt_all);
+    int eq_at = block_scan(lane == 0 ? eq : 0, scratch, &eq_all);
+    int* team2 = counts + kScratchInts;                         // [team][2]
+    if (cut && tid == 0) { team2[2 * tr] = gt_all; team2[2 * tr + 1] = eq_all; }
+    grid.sync();
+    if (!cut) return;
+    if (warp < 2) {
+        int s = 0;
+        for (int r = lane; r < tr; r += 32) s += __ldcg(team2 + 2 * r + warp);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) before2[warp] = s;
+    }
+    __syncthreads();
+    gt_at = __shfl_sync(0xffffffffu, gt_at, 0) + before2[0];
+    eq_at = __shfl_sync(0xffffffffu, eq_at, 0) + before2[1];
+    const uint32_t lt = (1u << lane) - 1u;
+    for (int i0 = s0; i0 < s1; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t u = i < s1 ? keys[i] : 0u;
+        const uint32_t mg = __ballot_sync(0xffffffffu, i < s1 && u > prefix);
+        const uint32_t me = __ballot_sync(0xffffffffu, i < s1 && u == prefix);
+        const int g = gt_at + __popc(mg & lt), e = eq_at + __popc(me & lt);
+        if (((mg >> lane) & 1u) || (((me >> lane) & 1u) && e < want)) idx[first + g + min(e, want)] = first + lo + i;
+        gt_at += __popc(mg);
+        eq_at += __popc(me);
+    }
+}
+
 // Rows to their new places.  ROW: bytes of a K (V) row; 16 bytes per lane, 512 / ROW rows of K
 // and V each per step of a warp, UN steps in flight.
 template <int ROW>
@@ -321,10 +462,7 @@ void move(const EvictArgs& a, int64_t keep, cudaStream_t st) {
     evict_move_kernel<ROW><<<static_cast<unsigned>(blocks) * a.batch, 256, 0, st>>>(a, keep, blocks);
 }
 
-}  // namespace
-
-cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
-    const int64_t keep = static_cast<int64_t>(a.sinks) + a.window + a.budget;
+cudaError_t select_cluster(const EvictArgs& a, cudaStream_t st) {
     // CTAs per sequence: as many as keep the batch on the SMs at once, up to the largest
     // cluster, and no more than leaves each a few thousand rows
     int cs = 1;
@@ -342,9 +480,39 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
     at[0].val.clusterDim.x = cs; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+}
+
+cudaError_t select_wide(const EvictArgs& a, int team, int row, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(evict_grid_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGridSmem);
     if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * team);
+    cfg.blockDim = dim3(ST);
+    cfg.dynamicSmemBytes = kGridSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeCooperative;
+    at[0].val.cooperative = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_grid_kernel, a, team, row);
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
+    const int64_t keep = static_cast<int64_t>(a.sinks) + a.window + a.budget;
     const int row = a.head_dim * (a.kv_dtype == HS2_F32 ? 4 : (a.kv_dtype == HS2_BF16 ? 2 : 1));
+    const int team = num_sms() / a.batch;
+    const int64_t slice = team > 0 ? (a.cap + team - 1) / team : a.cap;
+    // Teams of all SMs from 4096 rows on, unless k_out has no room for their counts.  Teams of a
+    // few CTAs with long slices gain nothing over clusters (32 x 64K rows: 51.3 us against 48.9;
+    // 16 x 32K: 43 against 63, 64 x 4K: 24.8 against 26.9, 1 x 1M: 73 against 109).
+    const bool wide = team > 1 && a.cap >= 4096 && slice <= kKeys && (team >= 8 || a.cap <= 32768) &&
+                      keep * row >= 4 * (kScratchInts + 2 * static_cast<int64_t>(team));
+    const cudaError_t e = wide ? select_wide(a, team, row, st) : select_cluster(a, st);
+    if (e != cudaSuccess) return e;
     if (row == 64) move<64>(a, keep, st);
     else if (row == 128) move<128>(a, keep, st);
     else if (row == 256) move<256>(a, keep, st);
