@@ -523,17 +523,17 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
 // and 16 zero rows (the end of a list is read to a multiple of 16).  8 codes of K and V per
 // thread and step.
 template <int D>
-__global__ void __launch_bounds__(256) window_widen_kernel(WindowArgs a, int s16, int64_t rows,
+__global__ void __launch_bounds__(256) window_widen_kernel(WindowArgs a, int blocks, int s16, int64_t rows,
                                                            __nv_bfloat16* __restrict__ kw, __nv_bfloat16* __restrict__ vw) {
     constexpr int PER = D / 8;
-    const int b = blockIdx.y;
+    const int b = blockIdx.x / blocks;
     const int live = live_rows(a.n_rows, b, a.n_q);
     if (live == 0) return;
     const int base = checked_base(a.q_pos0, b, live, a.max_ctx, a.status);
     const int lo = widened_lo(base, a.window, a.sinks), last = base + live - 1;
     const int64_t used = min(rows, static_cast<int64_t>(s16) + last - lo + 1 + 16);
-    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < used * PER; i += step) {
+    const int64_t step = static_cast<int64_t>(blocks) * blockDim.x;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x - b * blocks) * blockDim.x + threadIdx.x; i < used * PER; i += step) {
         const int64_t r = i / PER;
         const int c = static_cast<int>(i - r * PER);
         int key = -1;
@@ -581,8 +581,8 @@ cudaError_t launch(const WindowArgs& w, cudaStream_t st) {
         __nv_bfloat16* vw = kw + static_cast<size_t>(w.batch) * w.wide_rows * D;
         const int64_t work = (w.wide_rows * (D / 8) + 255) / 256;
         const int64_t most = 8 * static_cast<int64_t>(num_sms()) / w.batch + 1;
-        window_widen_kernel<D><<<dim3(static_cast<unsigned>(work < most ? work : most), w.batch), 256, 0, st>>>(
-            w, a.s16, w.wide_rows, kw, vw);
+        const int blocks = static_cast<int>(work < most ? work : most);
+        window_widen_kernel<D><<<static_cast<unsigned>(blocks) * w.batch, 256, 0, st>>>(w, blocks, a.s16, w.wide_rows, kw, vw);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         k = kw;

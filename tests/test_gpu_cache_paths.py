@@ -1,0 +1,227 @@
+"""GPU tests of the kernels behind the calls around the block at the sizes where one gives way to
+another: key lists cut over CTAs, narrow and wide weight items, clusters and teams of the
+eviction, rows shared by warps; values of very different magnitude; other streams.
+
+The forms, the checks and their tolerances are those of test_gpu_cache_ops.py."""
+import math
+
+import pytest
+import torch
+
+import cache_ops_ref as ref
+import kv_shared_b200 as hs
+import test_gpu_cache_ops as base
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ rows for the cache
+@pytest.mark.parametrize("b, n, h, d, rot, inter, dt, kv", [
+    (2, 330, 5, 128, 96, False, "bf16", "e4m3"), (1, 700, 3, 64, 32, True, "f32", "f32"),
+    (3, 250, 7, 64, 64, False, "bf16", "bf16"), (1, 640, 1, 128, 0, False, "f32", "e4m3"),
+    (2, 301, 24, 64, 48, False, "f32", "bf16"), (1, 601, 2, 128, 128, True, "bf16", "bf16"),
+])
+def test_rope_a_warp_to_a_row(b, n, h, d, rot, inter, dt, kv):
+    """Enough rows that each has one warp (fewer share a row between warps, as in the base tests)."""
+    base.test_rope_rows(b, n, h, d, rot, inter, dt, kv, True)
+
+
+# ------------------------------------------------------------------ sliding window
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("b, n, h, d, window, sinks, ctx", [
+    (1, 20, 16, 128, 3000, 4, 4000),       # few pairs, many keys: the keys of each tile are cut
+    (4, 33, 8, 64, 1500, 200, 2000),       # with a padded batch: parts without keys, sinks of over a tile
+    (1, 16, 16, 128, 128, 16, 300),        # one tile of exactly 256 pairs
+    (2, 17, 16, 128, 112, 15, 300),        # a pair of rows beyond it
+    (1, 24, 16, 64, 50, 120, 500),         # sinks longer than the window
+    (3, 26, 5, 128, 7, 1, 200),            # 130 pairs: the second half nearly empty
+    (1, 9, 128, 128, 1, 0, 40),            # a window of the row itself
+])
+def test_window_tiles(kv, b, n, h, d, window, sinks, ctx):
+    base._run_window(base._gen(n + ctx), b, n, h, d, window, sinks, ctx, kv, ragged=b == 4)
+
+
+@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("size", [1e-5, 1.0, 300.0])
+def test_window_e4m3_scales_of_many_magnitudes(n, size):
+    """Values whose rows differ by factors of thousands, queries far from one.  An output's error
+    is within 2^-8 of its weights' sum of |v|, whatever the rows' magnitudes."""
+    g = base._gen(n)
+    b, h, d, ctx, window = 2, 16, 128, 700, 600
+    q = (torch.randn(b, n, h, d, generator=g) * size).to(torch.bfloat16)
+    k = torch.randn(b, ctx, d, generator=g) / size
+    v = torch.randn(b, ctx, d, generator=g) * torch.exp2(torch.randint(-14, 15, (b, ctx, 1), generator=g).float())
+    (k, ks), (v, vs) = ref.quantize(k), ref.quantize(v)
+    pos0 = torch.tensor([ctx - n, 650 - n], dtype=torch.int32)
+    dev = base._cu(q, k, v, ks, vs, pos0, None)
+    o, lse = torch.zeros_like(dev[0]), torch.zeros(b, n, h, device="cuda")
+    desc = hs.make_desc(b, n, h, d, window=window, budget=0, kv_dtype=hs.HS2_E4M3, max_ctx=ctx)
+    ws = hs.alloc_window_workspace(desc, 3)
+    hs.hs2_window_attn(desc, 3, *dev, o, lse, ws)
+    assert hs.hs2_last_status(ws) == hs.HS2_OK
+    base._check_window(q, k, v, ks, vs, pos0, None, window, 3, o.cpu(), lse.cpu(), "e4m3", 0)
+
+
+# ------------------------------------------------------------------ accumulated weight
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("b, n, h, d, ctx", [
+    (1, 4, 16, 128, 600), (1, 5, 13, 128, 600),                # 64 and 65 pairs: one narrow tile, a wide one
+    (2, 1, 128, 64, 300), (1, 90, 16, 64, 90),                 # a prompt that scores itself: keys seen by some rows only
+    (4, 60, 16, 128, 200),                                     # pairs cut over CTAs, a padded batch
+    (1, 3, 1, 128, 1300), (1, 200, 3, 64, 1100),
+])
+def test_accum_narrow_wide_and_cut(kv, b, n, h, d, ctx):
+    base._run_accum(base._gen(n + ctx), b, n, h, d, ctx, kv, 0.5, ragged=b == 4)
+
+
+def test_accum_many_items_per_cta():
+    """More key blocks than SMs; totals against the plain form computed on the GPU in fp64."""
+    g = base._gen(3)
+    b, h, d = 2, 16, 128
+    for n, kv in ((1, "e4m3"), (1, "bf16"), (12, "bf16"), (12, "e4m3")):
+        ctx = 90001
+        q = torch.randn(b, n, h, d, generator=g).to(torch.bfloat16).cuda()
+        k, _, ks, _ = base._cache(g, b, ctx, d, kv)
+        kk = ref.wide(k, ks).cuda()
+        pos0 = torch.tensor([ctx - n, 70000], dtype=torch.int32, device="cuda")
+        x = torch.einsum("brhd,bkd->brhk", q.double(), kk) * d ** -0.5
+        hide = torch.arange(ctx, device="cuda") > (pos0[:, None] + torch.arange(n, device="cuda"))[..., None]
+        x = x.masked_fill(hide[:, :, None], -math.inf)
+        lse = x.logsumexp(-1).float()
+        want = (x - lse.double()[..., None]).exp().sum((1, 2))
+        acc = torch.full((b, ctx), 7.0, device="cuda")
+        desc = hs.make_desc(b, n, h, d, kv_dtype=base.KIND[kv], max_ctx=ctx)
+        ws = hs.alloc_accum_workspace(desc)
+        hs.hs2_weight_accum(desc, q, k.cuda(), None if ks is None else ks.cuda(), lse, pos0, None, 1.0, None, acc, ws)
+        assert hs.hs2_last_status(ws) == hs.HS2_OK
+        for s in range(b):
+            end = int(pos0[s]) + n
+            # logits up to 7: 2 d 2^-24 of the products' magnitudes (below 2^5) and the exponent's rounding
+            rel = (2 * d * 32 + 8 * 64) * 2.0 ** -24
+            assert (acc[s, :end].double() - want[s, :end]).abs().le(rel * want[s, :end] + 1e-30).all()
+            assert (acc[s, end:] == 7).all()
+
+
+@pytest.mark.parametrize("size", [1e-4, 1.0, 1e3])
+def test_accum_e4m3_queries_of_many_magnitudes(size):
+    """The query goes in as two e4m3 numbers per element: dims that differ by 2^10 stay exact."""
+    g = base._gen(17)
+    b, n, h, d, ctx = 1, 6, 16, 128, 500
+    q = (torch.randn(b, n, h, d, generator=g) * size * torch.exp2(-torch.randint(0, 9, (d,), generator=g).float())).to(torch.bfloat16)
+    k = torch.randn(b, ctx, d, generator=g) / size
+    k, ks = ref.quantize(k)
+    pos0 = torch.tensor([ctx - n], dtype=torch.int32)
+    kk = ref.wide(k[0], ks[0])
+    lse = torch.stack([((q[0, r].double() @ kk[:ctx - n + r + 1].T) * d ** -0.5).logsumexp(-1) for r in range(n)]).float()[None]
+    want, mag = ref.weight_total(q[0].double(), lse[0].double(), kk, ctx - n, d ** -0.5)
+    out = torch.zeros(b, ctx, device="cuda")
+    desc = hs.make_desc(b, n, h, d, kv_dtype=hs.HS2_E4M3, max_ctx=ctx)
+    ws = hs.alloc_accum_workspace(desc)
+    hs.hs2_weight_accum(desc, *base._cu(q, k, ks, lse, pos0, None), 1.0, None, out, ws)
+    rel = (2 * d * mag + 8 * (mag + 12)) * 2.0 ** -24 + 2.0 ** -20 + n * h * 2.0 ** -24
+    assert (out.cpu()[0].double() - want).abs().le(rel * want + 2.0 ** -22 * want).all()
+
+
+# ------------------------------------------------------------------ eviction
+def test_evict_teams_with_ties_and_specials():
+    """Slices in many CTAs: ties across them, NaN, infinities and zeros of both signs; counts above,
+    at and below the ties."""
+    g = base._gen(2)
+    few = torch.randint(0, 3, (2, 40000), generator=g).float()
+    few[1] = -few[1]
+    base._run_evict(few, [40000, 39001], 2, 10, 15000, "e4m3", 64)
+    odd = torch.randn(1, 9000, generator=g)
+    odd[0, ::7], odd[0, 1::7], odd[0, 2::7] = math.nan, math.inf, -math.inf
+    odd[0, 3::7], odd[0, 4::7] = 0.0, -0.0
+    for budget in (1285, 1290, 3000, 4500, 6500, 8990):
+        base._run_evict(odd, [9000], 0, 3, budget, "bf16", 128)
+    base._run_evict(torch.ones(3, 20000), [20000, 500, 12000], 1, 1, 9000, "bf16", 64, out_extra=2)
+    close = 1.0 + torch.randint(0, 3000, (1, 60000), generator=g).float() * 2.0 ** -23
+    base._run_evict(close, [60000], 1, 1, 23456, "f32", 64)
+
+
+def test_evict_clusters_with_long_lists():
+    """Few kept rows leave the counts no room beside them, so clusters select: with more equal totals
+    than their lists hold, and with lists."""
+    base._run_evict(torch.ones(1, 50000), [50000], 0, 2, 9, "e4m3", 64)
+    base._run_evict(torch.randint(0, 2, (2, 50000), generator=base._gen(1)).float(), [50000, 49000], 3, 0, 60, "e4m3", 64)
+    base._run_evict(torch.rand(1, 100000, generator=base._gen(5)), [100000], 0, 0, 90, "e4m3", 64)
+
+
+def test_evict_many_sequences():
+    acc = torch.rand(150, 300, generator=base._gen(6))
+    base._run_evict(acc, [300 - i for i in range(150)], 1, 5, 50, "bf16", 64)
+
+
+# ------------------------------------------------------------------ streams
+def test_calls_on_two_streams_at_once():
+    """The same calls on two side streams, each with its own outputs and workspaces, give the bits of
+    calls made alone."""
+    g = base._gen(44)
+    b, h, d, ctx = 2, 16, 128, 6000
+    k, v = (torch.randn(b, ctx, d, generator=g).bfloat16().cuda() for _ in range(2))
+    acc0 = torch.rand(b, ctx, generator=g).cuda()
+    ln = torch.full((b,), ctx, dtype=torch.int32, device="cuda")
+    sets = []
+    for n in (1, 40, 1, 40):
+        q = torch.randn(b, n, h, d, generator=g).bfloat16().cuda()
+        pos0 = torch.full((b,), ctx - n, dtype=torch.int32, device="cuda")
+        desc = hs.make_desc(b, n, h, d, window=5000, budget=0, max_ctx=ctx)
+        ed = hs.make_evict_desc(b, d, sinks=4, window=96, budget=400, kv_capacity=ctx)
+        out = dict(o=torch.zeros_like(q), lse=torch.zeros(b, n, h, device="cuda"), acc=torch.zeros(b, ctx, device="cuda"),
+                   ko=torch.zeros(b, 500, d, device="cuda").bfloat16(), vo=torch.zeros(b, 500, d, device="cuda").bfloat16(),
+                   idx=torch.zeros(b, 500, dtype=torch.int32, device="cuda"), nl=torch.zeros(b, dtype=torch.int32, device="cuda"))
+        sets.append((q, pos0, desc, ed, hs.alloc_window_workspace(desc, 4), hs.alloc_accum_workspace(desc), out))
+
+    def run(s, stream):
+        q, pos0, desc, ed, ws, aws, out = s
+        hs.hs2_window_attn(desc, 4, q, k, v, None, None, pos0, None, out["o"], out["lse"], ws, stream=stream)
+        hs.hs2_weight_accum(desc, q, k, None, out["lse"], pos0, None, 0.5, acc0, out["acc"], aws, stream=stream)
+        hs.hs2_kv_evict(ed, ln, out["acc"], k, v, None, None, out["ko"], out["vo"], None, None, None, out["idx"], out["nl"],
+                        stream=stream)
+
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    for s in sets:
+        run(s, side[0])
+    torch.cuda.synchronize()
+    alone = [{key: t.clone() for key, t in s[-1].items()} for s in sets]
+    for s in sets:
+        for t in s[-1].values():
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i, s in enumerate(sets):
+            run(s, side[i % 2])
+    torch.cuda.synchronize()
+    for want, s in zip(alone, sets):
+        for key, t in s[-1].items():
+            assert torch.equal(t, want[key]), key
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured calls of one workspace, replayed in turn on one stream."""
+    g = base._gen(45)
+    b, h, d, ctx = 1, 16, 128, 9000
+    k, v = (torch.randn(b, ctx, d, generator=g).bfloat16().cuda() for _ in range(2))
+    desc = hs.make_desc(b, 1, h, d, window=8000, budget=0, max_ctx=ctx)
+    ws = hs.alloc_window_workspace(desc, 4)
+    qs = [torch.randn(b, 1, h, d, generator=g).bfloat16().cuda() for _ in range(2)]
+    pos0 = torch.tensor([ctx - 1], dtype=torch.int32, device="cuda")
+    outs, graphs, want = [], [], []
+    for q in qs:
+        o = torch.zeros_like(q)
+        hs.hs2_window_attn(desc, 4, q, k, v, None, None, pos0, None, o, None, ws)
+        torch.cuda.synchronize()
+        want.append(o.clone())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            hs.hs2_window_attn(desc, 4, q, k, v, None, None, pos0, None, o, None, ws)
+        outs.append(o)
+        graphs.append(graph)
+    for _ in range(3):
+        for o, graph in zip(outs, graphs):
+            o.zero_()
+            graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
