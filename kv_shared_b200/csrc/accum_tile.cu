@@ -274,6 +274,7 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
         // ---------------------------------------------------------------- TMA loads
         Ring kr, qr;
         uint32_t kfree = KS, qfree = QS;                       // slots never used so far need no wait
+        bool split = !KV8;                                     // Q's parts are there (the keys need not wait for them)
         for (Walk at = p.walk.at(blockIdx.x); ok && p.walk.in(at); p.walk.next(at)) {
             if (!w.get(p, at) || w.t0 == w.t1) continue;
             const int krow = static_cast<int>(w.b * a.cap) + w.j0, qrow = w.b * a.n_q * a.heads;
@@ -292,6 +293,10 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
                 if (!ok) break;
                 if (qfree > 0) --qfree;
                 else if (!(ok = warp_wait(&q_empty[qr.slot], qr.phase ^ 1u, &abort_flag, a.status))) break;
+                if (!split) {
+                    asm volatile("griddepcontrol.wait;" ::: "memory");
+                    split = true;
+                }
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&q_full[qr.slot], p.n_cols * Sh::QROW);
                     for (int c = 0; c < Sh::QBOXES; ++c)
@@ -304,6 +309,7 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
         }
     } else if (warp == NEXP + 1) {
         // ---------------------------------------------------------------- the pairs' lse
+        if (KV8) asm volatile("griddepcontrol.wait;" ::: "memory");
         for (Walk at = p.walk.at(blockIdx.x); ok && p.walk.in(at); p.walk.next(at)) {
             if (!w.get(p, at)) continue;
             const int64_t flat0 = static_cast<int64_t>(w.b) * a.n_q * a.heads;
@@ -403,6 +409,7 @@ __global__ void __launch_bounds__(NT, 1) accum_tile_kernel(const __grid_constant
 template <int D>
 __global__ void __launch_bounds__(256) accum_split_q_kernel(const __nv_bfloat16* __restrict__ q, int64_t rows,
                                                             uint8_t* __restrict__ out, float* __restrict__ scale) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");        // which wait for our end where they need it
     constexpr int PER = D / 16;                                // elements of a lane: 4 or 8
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
     const int l = threadIdx.x & 15;
@@ -473,8 +480,17 @@ cudaError_t launch(TileArgs& p, const CUtensorMap& km, const CUtensorMap& qm, cu
     const int64_t items = static_cast<int64_t>(p.walk.batch) * p.walk.tiles * p.walk.parts;
     const int grid = items < num_sms() ? static_cast<int>(items) : num_sms();
     p.walk.step = p.walk.at(grid);
-    accum_tile_kernel<D, KV8, NARROW><<<static_cast<unsigned>(grid), NT, smem, st>>>(km, qm, p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = KV8 ? 1 : 0;                                // after the kernel that splits Q
+    return cudaLaunchKernelEx(&cfg, accum_tile_kernel<D, KV8, NARROW>, km, qm, p);
 }
 
 template <int D, bool KV8>
