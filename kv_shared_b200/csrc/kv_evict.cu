@@ -3,19 +3,18 @@
 // Of a sequence's n rows the first `sinks`, the latest `window` and the `budget` largest
 // totals between them survive, in order.  Two launches:
 //
-//   select  one cluster of CTAs per sequence.  The totals' bit patterns, made to order like
-//           the values, are counted by their upper 11 bits: each CTA counts its slice into
-//           shared memory, the cluster adds the counts, and the digit in which the budget
-//           runs out follows.  A second pass over the slice counts what lies above that digit
-//           and lists what has it (a few per cent of the rows); the lower 21 bits are then
-//           found from the lists alone, by rounds of 11 and 10 bits.  With the exact threshold
-//           pattern T and how many equal to it are still wanted (the lowest rows), a last pass
-//           writes the survivors' rows in order.  No atomic decides a position, so equal calls
-//           give equal bits.  A list that overflows (many equal totals) is not used: the later
-//           rounds then run over the slice.
-//           Where clusters would leave SMs idle, the same is done by a team of SMs / batch CTAs per sequence that meet in grid-wide barriers (a
-//           cooperative launch) and hold their slices' patterns in shared memory; their counts
-//           meet in the sequence's rows of k_out, which the move then overwrites.
+//   select  The totals' bit patterns, made to order like the values, are counted by their upper
+//           11 bits, and the digit in which the budget runs out follows; the middle 11 and the
+//           lower 10 bits are found the same way among the rows that share the bits so far.
+//           With the exact threshold pattern T and how many equal to it are still wanted (the
+//           lowest rows), a last pass writes the survivors' rows in order.  No atomic decides a
+//           position, so equal calls give equal bits.  A sequence is one CTA's, a cluster's
+//           (counts added through distributed shared memory) or, where clusters leave SMs idle,
+//           that of a team of SMs / batch CTAs that meet in grid-wide barriers (a cooperative
+//           launch; their counts meet in the sequence's rows of k_out, which the move then
+//           overwrites).  The patterns stay in shared memory; slices too long for it (many
+//           sequences, each over 40960 rows a CTA) are read again, and only the rows that share
+//           the first digit are listed.
 //   move    one warp per few rows copies K, V, scales and totals to their new places.
 //
 // Bound by HBM: 4 bytes per row of the totals (read once from HBM, then from L2) and twice
@@ -34,6 +33,9 @@ constexpr int ST = 1024;                         // threads of a select CTA
 constexpr int SW = ST / 32;
 constexpr int BINS = 2048;
 constexpr int COPIES = 4;                        // of the first round's counts (warps share them in turn)
+// rows per sequence up to which one CTA selects (1 x 4000: 11.6 us against a cluster's 17.0;
+// 4 x 16384: 17.9 against 18.2, 1 x 20000: 18.8 against 17.2)
+constexpr int64_t kOneRows = 16384;
 constexpr int kMaxCluster = 16;                  // more than 8 is an opt-in
 constexpr int LIST = 12288;                      // rows of a CTA's slice in the threshold's digit
 constexpr int LD = 16;                           // totals in flight per lane
@@ -269,20 +271,24 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(EvictArgs a) {
     }
 }
 
-// The same by a team of `team` CTAs per sequence, slices in shared memory.
+// The same with the slices' patterns in shared memory, by `team` CTAs per sequence: one (ONE), a
+// cluster, or any number that meets in grid-wide barriers (GRID).
 constexpr int kKeys = 40960;                     // rows of a CTA's slice, at most
-constexpr int kGridSmem = (COPIES * BINS + kKeys) * 4;
-constexpr int kScratchInts = 3 * BINS;           // counts of the three rounds; then two per CTA
+constexpr int kTeamSmem = (COPIES * BINS + BINS + kKeys) * 4;
+constexpr int kScratchInts = 3 * BINS;           // GRID: counts of the three rounds; then two per CTA
+enum { ONE = 0, CLUSTER = 1, GRID = 2 };
 
-__global__ void __launch_bounds__(ST) evict_grid_kernel(EvictArgs a, int team, int row_bytes) {
-    cg::grid_group grid = cg::this_grid();
+template <int MODE>
+__global__ void __launch_bounds__(ST) evict_team_kernel(EvictArgs a, int team, int row_bytes) {
+    cg::cluster_group cluster = cg::this_cluster();
     const int b = blockIdx.x / team, tr = blockIdx.x - b * team;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     extern __shared__ int dyn[];
     int* hist = dyn;                                            // [COPIES][BINS]
-    uint32_t* keys = reinterpret_cast<uint32_t*>(hist + COPIES * BINS);   // [kKeys]
+    int* sums = hist + COPIES * BINS;                           // [BINS] over the team
+    uint32_t* keys = reinterpret_cast<uint32_t*>(sums + BINS);  // [kKeys]
     __shared__ int scratch[SW + 1];
-    __shared__ int digit, rest, before2[2];
+    __shared__ int digit, rest, count2[2], before2[2];
 
     const int64_t keep = static_cast<int64_t>(a.sinks) + a.window + a.budget;
     int64_t n64 = a.len[b];
@@ -290,23 +296,15 @@ __global__ void __launch_bounds__(ST) evict_grid_kernel(EvictArgs a, int team, i
     const int n = static_cast<int>(n64);
     const int kept = n < keep ? n : static_cast<int>(keep);
     int32_t* idx = a.idx + b * keep;
-    if (tr == 0 && tid == 0) a.new_len[b] = kept;
-    for (int64_t i = kept + tr * ST + tid; i < keep; i += team * ST) idx[i] = -1;
     const bool cut = n > keep && a.budget > 0;                  // the same in the whole team
     const int first = a.sinks, m = cut ? n - a.window - a.sinks : 0;
-    if (n <= keep) {
-        for (int i = tr * ST + tid; i < n; i += team * ST) idx[i] = i;
-    } else {
-        for (int i = tr * ST + tid; i < a.sinks; i += team * ST) idx[i] = i;
-        for (int i = tr * ST + tid; i < a.window; i += team * ST) idx[a.sinks + a.budget + i] = n - a.window + i;
-    }
     const int per = (m + team - 1) / team;
     const int lo = min(m, tr * per), mine = min(m, lo + per) - lo;
     const float* acc = a.acc + b * a.cap + first + lo;
-    // the sequence's rows of k_out: only where rows are cut, hence all of them written later
+    // GRID: the sequence's rows of k_out, only where rows are cut, hence all of them written later
     int* counts = reinterpret_cast<int*>(static_cast<uint8_t*>(a.k_out) + static_cast<int64_t>(b) * a.out_cap * row_bytes);
     for (int i = tid; i < COPIES * BINS; i += ST) hist[i] = 0;
-    if (cut)
+    if (MODE == GRID && cut)
         for (int i = tr * ST + tid; i < kScratchInts; i += team * ST) counts[i] = 0;
     __syncthreads();
     int* copy = hist + (warp % COPIES) * BINS;
@@ -322,10 +320,20 @@ __global__ void __launch_bounds__(ST) evict_grid_kernel(EvictArgs a, int team, i
                 atomicAdd(&copy[u >> 21], 1);
             }
     }
+    // what does not depend on the totals
+    if (tr == 0 && tid == 0) a.new_len[b] = kept;
+    for (int64_t i = kept + tr * ST + tid; i < keep; i += team * ST) idx[i] = -1;
+    if (n <= keep) {
+        for (int i = tr * ST + tid; i < n; i += team * ST) idx[i] = i;
+    } else {
+        for (int i = tr * ST + tid; i < a.sinks; i += team * ST) idx[i] = i;
+        for (int i = tr * ST + tid; i < a.window; i += team * ST) idx[a.sinks + a.budget + i] = n - a.window + i;
+    }
+    if (MODE != GRID && !cut) return;                           // the whole team
     __syncthreads();
-    grid.sync();                                                // the counts are zero
+    if (MODE == GRID) cg::this_grid().sync();                   // the counts are zero
     uint32_t prefix = 0;                                        // bits of T found so far
-    int want = a.budget;
+    int want = a.budget;                                        // still wanted among those that share them
 #pragma unroll 1
     for (int round = 0; round < 3; ++round) {
         const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0);
@@ -340,18 +348,37 @@ __global__ void __launch_bounds__(ST) evict_grid_kernel(EvictArgs a, int team, i
             }
             __syncthreads();
         }
-        if (cut)
-            for (int i = tid; i < BINS; i += ST) {
-                int c = hist[i];
-                if (round == 0)
+        for (int i = tid; i < BINS; i += ST) {
+            int c = hist[i];
+            if (round == 0)
 #pragma unroll
-                    for (int k = 1; k < COPIES; ++k) c += hist[k * BINS + i];
-                if (c) atomicAdd(&counts[round * BINS + i], c);
+                for (int k = 1; k < COPIES; ++k) c += hist[k * BINS + i];
+            if (MODE == ONE) sums[i] = c;
+            else if (MODE == CLUSTER) hist[i] = c;
+            else if (cut && c) atomicAdd(&counts[round * BINS + i], c);
+        }
+        if (MODE == ONE) {
+            __syncthreads();
+        } else if (MODE == CLUSTER) {
+            cluster.sync();
+            // every CTA adds up its share of the bins over the cluster and hands the sums to all
+            const int share = BINS / team;
+            for (int i = tid; i < share; i += ST) {
+                const int bin = tr * share + i;
+                int c = 0;
+                for (int r = 0; r < team; ++r) c += cluster.map_shared_rank(hist, r)[bin];
+                for (int r = 0; r < team; ++r) cluster.map_shared_rank(sums, r)[bin] = c;
             }
-        grid.sync();
+            cluster.sync();
+        } else {
+            cg::this_grid().sync();
+        }
         if (cut) {
-            // the digit in which the budget runs out: thread t has the bins 2047 - 2t and 2046 - 2t
-            const int2 c = __ldcg(reinterpret_cast<const int2*>(counts + round * BINS) + (BINS / 2 - 1 - tid));
+            // the digit in which the budget runs out, from the highest down: thread t has the bins
+            // 2047 - 2t and 2046 - 2t
+            const int at = BINS / 2 - 1 - tid;
+            const int2 c = MODE == GRID ? __ldcg(reinterpret_cast<const int2*>(counts + round * BINS) + at)
+                                        : reinterpret_cast<const int2*>(sums)[at];
             int total;
             const int over = block_scan(c.x + c.y, scratch, &total);
             if (over < want && over + c.y >= want) { digit = BINS - 1 - 2 * tid; rest = want - over; }
@@ -362,8 +389,8 @@ __global__ void __launch_bounds__(ST) evict_grid_kernel(EvictArgs a, int team, i
             __syncthreads();
         }
     }
-    // rows above T = prefix and equal to it: of this warp's part of the slice, of the CTA, of the
-    // CTAs before
+    // rows above T = prefix and equal to it (the first `want` of which are kept): of this warp's
+    // part of the slice, of the CTA, of the CTAs before
     const int seg = ((mine + SW - 1) / SW + 31) & ~31;          // whole warps wide
     const int s0 = min(mine, warp * seg), s1 = min(mine, s0 + seg);
     int gt = 0, eq = 0;
@@ -380,20 +407,30 @@ __global__ void __launch_bounds__(ST) evict_grid_kernel(EvictArgs a, int team, i
     int gt_all, eq_all;
     int gt_at = block_scan(lane == 0 ? gt : 0, scratch, &gt_all);
     int eq_at = block_scan(lane == 0 ? eq : 0, scratch, &eq_all);
-    int* team2 = counts + kScratchInts;                         // [team][2]
-    if (cut && tid == 0) { team2[2 * tr] = gt_all; team2[2 * tr + 1] = eq_all; }
-    grid.sync();
-    if (!cut) return;
-    if (warp < 2) {
-        int s = 0;
-        for (int r = lane; r < tr; r += 32) s += __ldcg(team2 + 2 * r + warp);
+    gt_at = __shfl_sync(0xffffffffu, gt_at, 0);
+    eq_at = __shfl_sync(0xffffffffu, eq_at, 0);
+    if (MODE != ONE) {
+        int* team2 = counts + kScratchInts;                     // GRID: [team][2]
+        if (cut && tid == 0) {
+            if (MODE == GRID) { team2[2 * tr] = gt_all; team2[2 * tr + 1] = eq_all; }
+            else { count2[0] = gt_all; count2[1] = eq_all; }
+        }
+        if (MODE == GRID) cg::this_grid().sync();
+        else cluster.sync();
+        if (!cut) return;
+        if (warp < 2) {
+            int c = 0;
+            for (int r = lane; r < tr; r += 32)
+                c += MODE == GRID ? __ldcg(team2 + 2 * r + warp) : cluster.map_shared_rank(count2, r)[warp];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) before2[warp] = s;
+            for (int o = 16; o; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+            if (lane == 0) before2[warp] = c;
+        }
+        if (MODE == CLUSTER) cluster.sync();                    // also: no CTA leaves while it is read
+        else __syncthreads();
+        gt_at += before2[0];
+        eq_at += before2[1];
     }
-    __syncthreads();
-    gt_at = __shfl_sync(0xffffffffu, gt_at, 0) + before2[0];
-    eq_at = __shfl_sync(0xffffffffu, eq_at, 0) + before2[1];
     const uint32_t lt = (1u << lane) - 1u;
     for (int i0 = s0; i0 < s1; i0 += 32) {
         const int i = i0 + lane;
@@ -462,41 +499,54 @@ void move(const EvictArgs& a, int64_t keep, cudaStream_t st) {
     evict_move_kernel<ROW><<<static_cast<unsigned>(blocks) * a.batch, 256, 0, st>>>(a, keep, blocks);
 }
 
-cudaError_t select_cluster(const EvictArgs& a, cudaStream_t st) {
-    // CTAs per sequence: as many as keep the batch on the SMs at once, up to the largest
-    // cluster, and no more than leaves each a few thousand rows
+// CTAs per sequence of a cluster: as many as keep the batch on the SMs at once, up to the
+// largest cluster, and no more than leaves each a few thousand rows.
+int cluster_size(const EvictArgs& a) {
     int cs = 1;
     while (cs < kMaxCluster && 2 * cs * a.batch <= num_sms() && a.cap > static_cast<int64_t>(cs) * 4096) cs *= 2;
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * cs);
-    cfg.blockDim = dim3(ST);
-    cfg.dynamicSmemBytes = kSelectSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = cs; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+    return cs;
 }
 
-cudaError_t select_wide(const EvictArgs& a, int team, int row, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(evict_grid_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGridSmem);
+template <typename Kernel, typename... Args>
+cudaError_t launch_select(Kernel kernel, int grid, int smem, cudaLaunchAttribute at, cudaStream_t st, Args... args) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * team);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(ST);
-    cfg.dynamicSmemBytes = kGridSmem;
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeCooperative;
-    at[0].val.cooperative = 1;
-    cfg.attrs = at;
+    cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_grid_kernel, a, team, row);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+cudaError_t select(const EvictArgs& a, int64_t keep, int row, cudaStream_t st) {
+    cudaLaunchAttribute cluster{}, coop{};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    coop.id = cudaLaunchAttributeCooperative;
+    coop.val.cooperative = 1;
+    if (a.cap <= kOneRows) {
+        cluster.val.clusterDim.x = 1;
+        return launch_select(evict_team_kernel<ONE>, a.batch, kTeamSmem, cluster, st, a, 1, row);
+    }
+    // Teams of all SMs where a cluster's slices are long and SMs idle, or where large clusters do
+    // not all fit at once (a GPC takes one or two of 8), unless k_out has no room for their counts.
+    // Measured, the whole call, teams against clusters: 1 x 1M e4m3 rows 74 us against 108, 2 x 256K
+    // bf16 43.5 against 45.4, 8 x 128K 47 against 60, 16 x 32K 44 against 52; the other way
+    // 1 x 64K 21.7 against 19.6, 4 x 64K 23.2 against 21.5, 32 x 32K 26.6 against 21.9.
+    const int team = num_sms() / a.batch, cs = cluster_size(a);
+    const int64_t slice = team > 0 ? (a.cap + team - 1) / team : a.cap;
+    const bool idle = team >= 2 * cs && a.cap > static_cast<int64_t>(cs) * 8192, crowd = cs >= 8 && a.batch * cs > 64;
+    if (team > 1 && slice <= kKeys && (idle || crowd) &&
+        keep * row >= 4 * (kScratchInts + 2 * static_cast<int64_t>(team)))
+        return launch_select(evict_team_kernel<GRID>, a.batch * team, kTeamSmem, coop, st, a, team, row);
+    cluster.val.clusterDim.x = cs;
+    if ((a.cap + cs - 1) / cs <= kKeys)
+        return launch_select(evict_team_kernel<CLUSTER>, a.batch * cs, kTeamSmem, cluster, st, a, cs, row);
+    return launch_select(evict_select_kernel, a.batch * cs, kSelectSmem, cluster, st, a);
 }
 
 }  // namespace
@@ -504,14 +554,7 @@ cudaError_t select_wide(const EvictArgs& a, int team, int row, cudaStream_t st) 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
     const int64_t keep = static_cast<int64_t>(a.sinks) + a.window + a.budget;
     const int row = a.head_dim * (a.kv_dtype == HS2_F32 ? 4 : (a.kv_dtype == HS2_BF16 ? 2 : 1));
-    const int team = num_sms() / a.batch;
-    const int64_t slice = team > 0 ? (a.cap + team - 1) / team : a.cap;
-    // Teams of all SMs from 4096 rows on, unless k_out has no room for their counts.  Teams of a
-    // few CTAs with long slices gain nothing over clusters (32 x 64K rows: 51.3 us against 48.9;
-    // 16 x 32K: 43 against 63, 64 x 4K: 24.8 against 26.9, 1 x 1M: 73 against 109).
-    const bool wide = team > 1 && a.cap >= 4096 && slice <= kKeys && (team >= 8 || a.cap <= 32768) &&
-                      keep * row >= 4 * (kScratchInts + 2 * static_cast<int64_t>(team));
-    const cudaError_t e = wide ? select_wide(a, team, row, st) : select_cluster(a, st);
+    const cudaError_t e = select(a, keep, row, st);
     if (e != cudaSuccess) return e;
     if (row == 64) move<64>(a, keep, st);
     else if (row == 128) move<128>(a, keep, st);

@@ -123,29 +123,37 @@ def test_accum_e4m3_queries_of_many_magnitudes(size):
 
 
 # ------------------------------------------------------------------ eviction
-def test_evict_teams_with_ties_and_specials():
-    """Slices in many CTAs: ties across them, NaN, infinities and zeros of both signs; counts above,
-    at and below the ties."""
-    g = base._gen(2)
-    few = torch.randint(0, 3, (2, 40000), generator=g).float()
-    few[1] = -few[1]
-    base._run_evict(few, [40000, 39001], 2, 10, 15000, "e4m3", 64)
-    odd = torch.randn(1, 9000, generator=g)
+@pytest.mark.parametrize("lens", [[9000], [20000, 19000], [70000] * 3, [300000, 299999], [40000] * 16])
+def test_evict_one_cta_clusters_and_teams(lens):
+    """One CTA, clusters of 8 and 16, teams of all SMs: ties across slices, NaN, infinities and zeros of
+    both signs, counts above, at and below the ties, a last-bit difference."""
+    b, cap = len(lens), max(lens)
+    g = base._gen(cap)
+    few = torch.randint(0, 3, (b, cap), generator=g).float()
+    few[::2] = -few[::2]
+    base._run_evict(few, lens, 2, 10, cap // 3 + 5, "e4m3", 64)
+    odd = torch.randn(b, cap, generator=g)
+    odd[:, ::7], odd[:, 1::7], odd[:, 2::7] = math.nan, math.inf, -math.inf
+    odd[:, 3::7], odd[:, 4::7] = 0.0, -0.0
+    base._run_evict(odd, lens, 0, 3, cap * 3 // 7, "bf16", 64)
+    close = 1.0 + torch.randint(0, 3000, (b, cap), generator=g).float() * 2.0 ** -23
+    base._run_evict(close, [max(1, n - 3000 * i) for i, n in enumerate(lens)], 1, 1, cap // 5, "e4m3", 64, out_extra=2)
+
+
+def test_evict_kept_rows_around_the_ties():
+    odd = torch.randn(1, 30000, generator=base._gen(2))
     odd[0, ::7], odd[0, 1::7], odd[0, 2::7] = math.nan, math.inf, -math.inf
     odd[0, 3::7], odd[0, 4::7] = 0.0, -0.0
-    for budget in (1285, 1290, 3000, 4500, 6500, 8990):
-        base._run_evict(odd, [9000], 0, 3, budget, "bf16", 128)
-    base._run_evict(torch.ones(3, 20000), [20000, 500, 12000], 1, 1, 9000, "bf16", 64, out_extra=2)
-    close = 1.0 + torch.randint(0, 3000, (1, 60000), generator=g).float() * 2.0 ** -23
-    base._run_evict(close, [60000], 1, 1, 23456, "f32", 64)
+    for budget in (1, 4285, 4286, 8000, 12850, 17140, 21430, 29980):
+        base._run_evict(odd, [30000], 0, 3, budget, "bf16", 64)
 
 
-def test_evict_clusters_with_long_lists():
-    """Few kept rows leave the counts no room beside them, so clusters select: with more equal totals
-    than their lists hold, and with lists."""
-    base._run_evict(torch.ones(1, 50000), [50000], 0, 2, 9, "e4m3", 64)
-    base._run_evict(torch.randint(0, 2, (2, 50000), generator=base._gen(1)).float(), [50000, 49000], 3, 0, 60, "e4m3", 64)
-    base._run_evict(torch.rand(1, 100000, generator=base._gen(5)), [100000], 0, 0, 90, "e4m3", 64)
+def test_evict_long_slices_are_read_again():
+    """More rows a CTA than shared memory holds: few kept rows (no room for counts beside them) of a
+    long cache, with more equal totals than the lists take, and with lists."""
+    base._run_evict(torch.ones(1, 700000), [700000], 0, 2, 9, "e4m3", 64)
+    base._run_evict(torch.randint(0, 2, (1, 700000), generator=base._gen(1)).float(), [699000], 3, 0, 60, "e4m3", 64)
+    base._run_evict(torch.rand(1, 700001, generator=base._gen(5)), [700001], 0, 0, 90, "e4m3", 64)
 
 
 def test_evict_many_sequences():
