@@ -32,7 +32,7 @@ constexpr int F_QT = 8;                          // fp32: threads that share two
 constexpr int F_ROWS = 2 * 128 / F_QT;           // (row, head) pairs per CTA
 constexpr int F_KEYS = 32;                       // keys per tile
 constexpr int kMinSplitKeysF32 = 256;
-constexpr int64_t kTilePairs = 129;               // (row, head) pairs per sequence from which the tcgen05 kernel is taken
+constexpr int kMinSplitKeysTile = 256;
 
 template <int D, bool KV8>
 struct Frag {
@@ -621,21 +621,48 @@ cudaError_t launch_join(const WindowArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+namespace {
+
+// One kernel's launch: (row, head) pairs and keys per CTA, parts the keys are cut into, rounds of
+// CTAs on the SMs.
+struct Shape {
+    int64_t tiles, keys, parts, rounds;
+};
+Shape shape(int batch, int64_t pairs, int heads, int window, int sinks, int64_t max_ctx, int rows, int per_sm, int min_keys) {
+    Shape s;
+    s.tiles = (pairs + rows - 1) / rows * batch;
+    // keys of a tile: its rows' windows and the sinks, at most the whole context
+    s.keys = static_cast<int64_t>(window) + rows / heads + sinks + kSinkPad;
+    if (s.keys > max_ctx + kSinkPad) s.keys = max_ctx + kSinkPad;
+    // parts: as many as fill the SMs once, each with enough keys to be worth the join
+    s.parts = num_sms() * per_sm / s.tiles;
+    if (s.parts > s.keys / min_keys) s.parts = s.keys / min_keys;
+    if (s.parts < 1) s.parts = 1;
+    s.rounds = (s.tiles * s.parts + num_sms() * per_sm - 1) / (num_sms() * per_sm);
+    return s;
+}
+
+}  // namespace
+
 WindowPlan plan_window(int batch, int n_q, int heads, int kv_dtype, int window, int sinks, int64_t max_ctx) {
-    const bool f32 = kv_dtype == HS2_F32;
     const int64_t pairs = static_cast<int64_t>(n_q) * heads;
     WindowPlan p{};
-    p.tile = !f32 && pairs >= kTilePairs;
-    const int rows = f32 ? F_ROWS : (p.tile ? 256 : 16);
-    const int64_t tiles = (pairs + rows - 1) / rows * batch;
-    // keys of a tile: its rows' windows and the sinks, at most the whole context
-    int64_t keys = static_cast<int64_t>(window) + rows / heads + sinks + kSinkPad;
-    if (keys > max_ctx + kSinkPad) keys = max_ctx + kSinkPad;
-    // parts: as many as fill the SMs once, each with enough keys to be worth the join
-    int64_t s = num_sms() * (f32 ? 2 : 1) / tiles;
-    const int64_t most = keys / (f32 ? kMinSplitKeysF32 : kMinSplitKeys);
-    if (s > most) s = most;
-    p.splits = s < 1 ? 1 : static_cast<int>(s);
+    if (kv_dtype == HS2_F32) {
+        p.splits = static_cast<int>(shape(batch, pairs, heads, window, sinks, max_ctx, F_ROWS, 2, kMinSplitKeysF32).parts);
+        return p;
+    }
+    const Shape r = shape(batch, pairs, heads, window, sinks, max_ctx, 16, 1, kMinSplitKeys);
+    const Shape t = shape(batch, pairs, heads, window, sinks, max_ctx, 256, 1, kMinSplitKeysTile);
+    // The tcgen05 kernel is the faster one per key but slow to start and to join, so the small
+    // calls are left to the other.  Both estimated, in tenths of a microsecond, from what they
+    // measured (bf16, 16 heads; rows kernel against tile kernel): 64 rows, window 128: 5.9 us
+    // against 11.6; 8 x 64 rows: 19.4 against 11.8; 4 x 64 rows, window 1000: 23.6 against 38.5;
+    // 256 rows, window 4000: 71 against 41; 8192 rows: 1350 against 120.
+    const int64_t cost_r = 40 + r.rounds * (9 * ((r.keys / r.parts + 127) / 128) + 20) + (r.parts > 1 ? 50 : 0);
+    const int64_t cost_t = 80 + t.rounds * 35 * ((t.keys / t.parts + 127) / 128) +
+                           (t.parts > 1 ? 50 + batch * pairs * t.parts / 500 : 0);
+    p.tile = pairs > 16 && cost_t < cost_r;
+    p.splits = static_cast<int>(p.tile ? t.parts : r.parts);
     if (p.tile && kv_dtype == HS2_E4M3) p.wide_rows = window_wide_rows(n_q, window, sinks, max_ctx);
     return p;
 }

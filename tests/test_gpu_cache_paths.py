@@ -29,25 +29,75 @@ def test_rope_a_warp_to_a_row(b, n, h, d, rot, inter, dt, kv):
 # ------------------------------------------------------------------ sliding window
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("b, n, h, d, window, sinks, ctx", [
-    (1, 20, 16, 128, 3000, 4, 4000),       # few pairs, many keys: the keys of each tile are cut
+    (1, 20, 16, 128, 3000, 4, 4000),       # few pairs, many keys: the keys are cut
     (4, 33, 8, 64, 1500, 200, 2000),       # with a padded batch: parts without keys, sinks of over a tile
-    (1, 16, 16, 128, 128, 16, 300),        # one tile of exactly 256 pairs
-    (2, 17, 16, 128, 112, 15, 300),        # a pair of rows beyond it
+    (1, 16, 16, 128, 128, 16, 300), (2, 17, 16, 128, 112, 15, 300),
     (1, 24, 16, 64, 50, 120, 500),         # sinks longer than the window
-    (3, 26, 5, 128, 7, 1, 200),            # 130 pairs: the second half nearly empty
+    (3, 26, 5, 128, 7, 1, 200),
     (1, 9, 128, 128, 1, 0, 40),            # a window of the row itself
 ])
-def test_window_tiles(kv, b, n, h, d, window, sinks, ctx):
+def test_window_small_calls(kv, b, n, h, d, window, sinks, ctx):
     base._run_window(base._gen(n + ctx), b, n, h, d, window, sinks, ctx, kv, ragged=b == 4)
 
 
-@pytest.mark.parametrize("n", [1, 20])
+# calls large enough for the tcgen05 kernel
+LARGE = [
+    # b, n, h, d, window, sinks, ctx
+    (1, 512, 16, 128, 128, 4, 900), (3, 340, 8, 64, 33, 130, 700), (2, 8200, 1, 64, 1, 0, 8300),
+    (2, 900, 5, 128, 64, 16, 1300), (1, 90, 128, 128, 30, 3, 200), (1, 520, 16, 64, 50, 120, 600),
+    (1, 257, 16, 128, 3000, 4, 4000),      # keys cut
+    (4, 80, 16, 128, 2500, 20, 4000),      # keys cut, a padded batch: sequences of no rows, parts of no keys
+    (4, 300, 16, 64, 100, 15, 1000), (1, 600, 16, 128, 1 << 30, 7, 600), (2, 400, 12, 128, 112, 16, 500),
+]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("b, n, h, d, window, sinks, ctx", LARGE)
+def test_window_large_calls(kv, b, n, h, d, window, sinks, ctx):
+    rows = sorted({0, 1, 2, 7, 8, 15, 16, 17, 31, 32, 50, 51, 52, n // 2 - 1, n // 2, n - 17, n - 2, n - 1})
+    base._run_window(base._gen(n + ctx), b, n, h, d, window, sinks, ctx, kv, ragged=b == 4, rows=rows)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_window_large_call_with_rising_logits(kv):
+    """Logits of several hundred that rise along the keys, so that the reference moves at every tile."""
+    g = base._gen(9)
+    b, n, h, d, ctx = 1, 600, 16, 128, 1400
+    q = (torch.randn(b, n, h, d, generator=g) * 16).to(torch.bfloat16)
+    k = torch.randn(b, ctx, d, generator=g) * 4
+    k = k[:, torch.argsort(k[0] @ q[0, 0, 0].float())]
+    v = torch.randn(b, ctx, d, generator=g) + 1e4
+    (k, ks), (v, vs) = (ref.quantize(k), ref.quantize(v)) if kv == "e4m3" else ((k.bfloat16(), None), (v.bfloat16(), None))
+    pos0 = torch.tensor([ctx - n], dtype=torch.int32)
+    dev = base._cu(q, k, v, ks, vs, pos0, None)
+    o, lse = torch.zeros_like(dev[0]), torch.zeros(b, n, h, device="cuda")
+    desc = hs.make_desc(b, n, h, d, window=900, budget=0, kv_dtype=base.KIND[kv], max_ctx=ctx)
+    ws = hs.alloc_window_workspace(desc, 2)
+    hs.hs2_window_attn(desc, 2, *dev, o, lse, ws)
+    assert hs.hs2_last_status(ws) == hs.HS2_OK
+    base._check_window(q, k, v, ks, vs, pos0, None, 900, 2, o.cpu(), lse.cpu(), kv, 0, rows=[0, 1, 100, 333, 598, 599])
+
+
+def test_window_large_call_reports_positions_outside_the_context():
+    desc = hs.make_desc(2, 600, 16, 128, window=128, budget=0, max_ctx=700)
+    ws = hs.alloc_window_workspace(desc, 1)
+    q = torch.randn(2, 600, 16, 128, device="cuda").bfloat16()
+    kv = torch.randn(2, 700, 128, device="cuda").bfloat16()
+    o = torch.zeros_like(q)
+    for bad in ([-1, 0], [0, 101]):
+        pos0 = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        hs.hs2_window_attn(desc, 1, q, kv, kv, None, None, pos0, None, o, None, ws)
+        assert hs.hs2_last_status(ws) == hs.HS2_ERR_INDEX
+    assert hs.hs2_last_status(ws) == hs.HS2_OK
+
+
+@pytest.mark.parametrize("n", [1, 20, 600])
 @pytest.mark.parametrize("size", [1e-5, 1.0, 300.0])
 def test_window_e4m3_scales_of_many_magnitudes(n, size):
     """Values whose rows differ by factors of thousands, queries far from one.  An output's error
     is within 2^-8 of its weights' sum of |v|, whatever the rows' magnitudes."""
     g = base._gen(n)
-    b, h, d, ctx, window = 2, 16, 128, 700, 600
+    b, h, d, ctx, window = 2, 16, 128, 1300, 600
     q = (torch.randn(b, n, h, d, generator=g) * size).to(torch.bfloat16)
     k = torch.randn(b, ctx, d, generator=g) / size
     v = torch.randn(b, ctx, d, generator=g) * torch.exp2(torch.randint(-14, 15, (b, ctx, 1), generator=g).float())
@@ -59,7 +109,7 @@ def test_window_e4m3_scales_of_many_magnitudes(n, size):
     ws = hs.alloc_window_workspace(desc, 3)
     hs.hs2_window_attn(desc, 3, *dev, o, lse, ws)
     assert hs.hs2_last_status(ws) == hs.HS2_OK
-    base._check_window(q, k, v, ks, vs, pos0, None, window, 3, o.cpu(), lse.cpu(), "e4m3", 0)
+    base._check_window(q, k, v, ks, vs, pos0, None, window, 3, o.cpu(), lse.cpu(), "e4m3", 0, rows=[0, 1, 19, 300, 599])
 
 
 # ------------------------------------------------------------------ accumulated weight
