@@ -355,7 +355,8 @@ HS2_API size_t hs2_weight_accum_workspace_size(const hs2_attn_desc* desc);
  * were.  q and lse are a full-attention call's query and its lse output (the last
  * rows of a prompt alone, or one new token, are ordinary uses).  acc_in, acc_out:
  * [batch][kv_capacity] fp32; acc_in may be acc_out, or NULL for zeros (decay is then
- * unused); decay >= 0.  desc->window, budget and idx_stride are not used.  The sums'
+ * unused); decay >= 0.  E4M3 caches: query elements below 2^-9 of their row's largest are
+ * rounded to 2^-17 of it.  desc->window, budget and idx_stride are not used.  The sums'
  * order is fixed by the sizes: equal calls give equal bits.
  */
 HS2_API hs2_status hs2_weight_accum(const hs2_attn_desc* desc, const void* q, const void* k,

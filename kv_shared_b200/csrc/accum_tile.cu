@@ -24,8 +24,11 @@
 // e4m3 caches: the codes are the MMA's operand as they lie in the cache.  Q goes in as a sum of
 // two e4m3 numbers, found once per call: q 2^e = hi + lo with the row's largest magnitude in
 // [128, 256).  bf16 has 8 significant bits and e4m3 4, so hi takes the upper and lo the lower
-// ones exactly, down to elements 2^-10 of the row's largest; what is lost below that is at
-// most 2^-18 of the largest, under the fp32 error of the products with it.
+// ones exactly, down to elements 2^-9 of the row's largest; smaller ones are rounded to 2^-17
+// of it at worst.
+//
+// Measured: 32 rows of 16 heads over 4 x 131072 bf16 keys 93 us (740 TFLOP/s; exponentials and
+// their arithmetic alone would take 50), one row over 8 x 100001 e4m3 keys 25.9 us (4.3 TB/s).
 //
 // Roles (640 threads): warps 0-15 exponentials, 16 the TMA loads, 17 the pairs' lse (and
 // scales), 18 and 19 the MMAs of the even and the odd 128 keys.  Every wait is bounded; a

@@ -17,8 +17,8 @@
 //           the first digit are listed.
 //   move    one warp per few rows copies K, V, scales and totals to their new places.
 //
-// Bound by HBM: 4 bytes per row of the totals (read once from HBM, then from L2) and twice
-// the surviving rows' bytes.
+// The move is bound by HBM (twice the surviving rows' bytes: 525,000 e4m3 rows 50 us, 32 x 4228
+// bf16 rows 24.6 us), the selection by its barriers (5 to 9 us for one CTA, 22 us for 1M rows or 32 x 64K).
 #include <cooperative_groups.h>
 
 #include "common.cuh"

@@ -11,7 +11,8 @@
 // angles are multiplied once and serve every query head of the row, two dims to an
 // instruction; the key and the value, one of each, go their own way at the end.  (All vectors
 // on one path, chosen by selection: 86 us for 4 x 8192 rows of 16 heads of 128.)  The angles
-// depend on the row alone and are formed by its warp: position times frequency in turns in fp64, the whole
+// depend on the row alone and are formed by its warp (measured: 4 x 8192 rows of 16 heads of 128
+// 57.6 us, 5.2 TB/s; 32 single rows 3.2 us): position times frequency in turns in fp64, the whole
 // turns dropped there, so that a position of a million loses nothing, then sine and cosine of
 // the fraction in fp32.
 #include "common.cuh"

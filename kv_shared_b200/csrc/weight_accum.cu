@@ -20,7 +20,8 @@ constexpr int S_ROWS = 32;                       // (row, head) pairs per tile
 __device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 
 // fp32 caches on the CUDA cores.  Thread (kp, qt) of 32 x 4 has keys 2 kp, 2 kp + 1 and the
-// pairs qt + 4 i of a tile.
+// pairs qt + 4 i of a tile.  Bound by the fp32 FMAs and the shared-memory loads
+// between them (10 of 16 bytes to 64 FMAs).
 template <int D>
 __global__ void __launch_bounds__(128) accum_f32_kernel(AccumArgs a) {
     constexpr int LD = D + 4;
