@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(EvictArgs a) {
 // The same with the slices' patterns in shared memory, by `team` CTAs per sequence: one (ONE), a
 // cluster, or any number that meets in grid-wide barriers (GRID).
 constexpr int kKeys = 40960;                     // rows of a CTA's slice, at most
-constexpr int kTeamSmem = (COPIES * BINS + BINS + kKeys) * 4;
+constexpr int team_smem(int64_t slice) { return static_cast<int>((COPIES * BINS + BINS + slice) * 4); }
 constexpr int kScratchInts = 3 * BINS;           // GRID: counts of the three rounds; then two per CTA
 enum { ONE = 0, CLUSTER = 1, GRID = 2 };
 
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(ST) evict_team_kernel(EvictArgs a, int team, i
     extern __shared__ int dyn[];
     int* hist = dyn;                                            // [COPIES][BINS]
     int* sums = hist + COPIES * BINS;                           // [BINS] over the team
-    uint32_t* keys = reinterpret_cast<uint32_t*>(sums + BINS);  // [kKeys]
+    uint32_t* keys = reinterpret_cast<uint32_t*>(sums + BINS);  // [slice]
     __shared__ int scratch[SW + 1];
     __shared__ int digit, rest, count2[2], before2[2];
 
@@ -530,7 +530,7 @@ cudaError_t select(const EvictArgs& a, int64_t keep, int row, cudaStream_t st) {
     coop.val.cooperative = 1;
     if (a.cap <= kOneRows) {
         cluster.val.clusterDim.x = 1;
-        return launch_select(evict_team_kernel<ONE>, a.batch, kTeamSmem, cluster, st, a, 1, row);
+        return launch_select(evict_team_kernel<ONE>, a.batch, team_smem(a.cap), cluster, st, a, 1, row);
     }
     // Teams of all SMs where a cluster's slices are long and SMs idle, or where large clusters do
     // not all fit at once (a GPC takes one or two of 8), unless k_out has no room for their counts.
@@ -542,10 +542,11 @@ cudaError_t select(const EvictArgs& a, int64_t keep, int row, cudaStream_t st) {
     const bool idle = team >= 2 * cs && a.cap > static_cast<int64_t>(cs) * 8192, crowd = cs >= 8 && a.batch * cs > 64;
     if (team > 1 && slice <= kKeys && (idle || crowd) &&
         keep * row >= 4 * (kScratchInts + 2 * static_cast<int64_t>(team)))
-        return launch_select(evict_team_kernel<GRID>, a.batch * team, kTeamSmem, coop, st, a, team, row);
+        return launch_select(evict_team_kernel<GRID>, a.batch * team, team_smem(slice), coop, st, a, team, row);
     cluster.val.clusterDim.x = cs;
-    if ((a.cap + cs - 1) / cs <= kKeys)
-        return launch_select(evict_team_kernel<CLUSTER>, a.batch * cs, kTeamSmem, cluster, st, a, cs, row);
+    const int64_t part = (a.cap + cs - 1) / cs;
+    if (part <= kKeys)
+        return launch_select(evict_team_kernel<CLUSTER>, a.batch * cs, team_smem(part), cluster, st, a, cs, row);
     return launch_select(evict_select_kernel, a.batch * cs, kSelectSmem, cluster, st, a);
 }
 

@@ -531,6 +531,9 @@ __global__ void __launch_bounds__(128) window_f32_kernel(WindowArgs a) {
 constexpr int JOIN_Y = 8;
 template <typename T, int D>
 __global__ void __launch_bounds__(D / 4 * JOIN_Y) window_join_kernel(WindowArgs a, FastDiv rows) {
+    // Launched early: the parts are there from here on.  Before any return, or a call of no rows
+    // would be over before the kernel ahead of it.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t all = static_cast<int64_t>(a.batch) * a.n_q * a.heads;
     const int64_t flat = blockIdx.x;
     const int b = rows.div(static_cast<int>(flat));              // rows.d: pairs per sequence
@@ -538,7 +541,6 @@ __global__ void __launch_bounds__(D / 4 * JOIN_Y) window_join_kernel(WindowArgs 
     const int d = threadIdx.x * 4, y = threadIdx.y;
     float mx = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    asm volatile("griddepcontrol.wait;" ::: "memory");          // launched early: the parts are there from here on
     constexpr int AHEAD = 5;                                     // parts in flight per thread
     for (int s0 = y; s0 < a.splits; s0 += JOIN_Y * AHEAD) {
         float2 ml[AHEAD];

@@ -206,6 +206,32 @@ def test_evict_long_slices_are_read_again():
     base._run_evict(torch.rand(1, 700001, generator=base._gen(5)), [700001], 0, 0, 90, "e4m3", 64)
 
 
+@pytest.mark.parametrize("n, kv", [(1, "bf16"), (1, "e4m3"), (20, "bf16"), (600, "bf16"), (600, "e4m3"), (3, "f32")])
+def test_calls_of_no_rows(n, kv):
+    """A padded batch without a row in use: outputs stay, totals fade, and what follows is not overtaken."""
+    g = base._gen(n)
+    b, h, d, ctx = 2, 16, 128, 9000
+    dt = base.DT["f32" if kv == "f32" else "bf16"]
+    q = torch.full((b, n, h, d), math.nan, dtype=dt, device="cuda")
+    k, v, ks, vs = base._cu(*base._cache(g, b, ctx, d, kv))
+    pos0 = torch.tensor([ctx - n, 100], dtype=torch.int32, device="cuda")
+    none = torch.zeros(b, dtype=torch.int32, device="cuda")
+    desc = hs.make_desc(b, n, h, d, window=8000, budget=0, q_dtype=base.KIND["f32" if kv == "f32" else "bf16"],
+                        kv_dtype=base.KIND[kv], max_ctx=ctx)
+    ws, aws = hs.alloc_window_workspace(desc, 4), hs.alloc_accum_workspace(desc)
+    o, lse = torch.full_like(q, 7.0), torch.full((b, n, h), math.nan, device="cuda")
+    acc = torch.rand(b, ctx, generator=g).cuda()
+    out = torch.full_like(acc, -3.0)
+    for _ in range(3):
+        hs.hs2_window_attn(desc, 4, q, k, v, ks, vs, pos0, none, o, lse, ws)
+        hs.hs2_weight_accum(desc, q, k, ks, lse, pos0, none, 0.5, acc, out, aws)
+    assert hs.hs2_last_status(ws) == hs.HS2_OK and hs.hs2_last_status(aws) == hs.HS2_OK
+    assert (o == 7).all() and lse.isnan().all()
+    for s in range(b):
+        p = int(pos0[s])
+        assert torch.equal(out[s, :p], 0.5 * acc[s, :p]) and (out[s, p:] == -3).all()
+
+
 def test_evict_many_sequences():
     acc = torch.rand(150, 300, generator=base._gen(6))
     base._run_evict(acc, [300 - i for i in range(150)], 1, 5, 50, "bf16", 64)
