@@ -15,19 +15,19 @@ namespace hs2 {
 namespace {
 
 constexpr int S_KEYS = 64;                       // keys per CTA
-constexpr int S_ROWS = 32;                       // (row, head) pairs per tile
 
 __device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 
-// fp32 caches on the CUDA cores.  Thread (kp, qt) of 32 x 4 has keys 2 kp, 2 kp + 1 and the
-// pairs qt + 4 i of a tile.  Bound by the fp32 FMAs and the shared-memory loads
+// fp32 caches on the CUDA cores.  Thread (kp, qt) of 32 x 4 has keys 2 kp, 2 kp + 1 and the PP
+// pairs qt + 4 i of a tile (8; 4 where a sequence has no more than 16).  Bound by the fp32 FMAs and the shared-memory loads
 // between them (10 of 16 bytes to 64 FMAs).
-template <int D>
+template <int D, int PP>
 __global__ void __launch_bounds__(128) accum_f32_kernel(AccumArgs a) {
+    constexpr int S_ROWS = 4 * PP;               // (row, head) pairs per tile
     constexpr int LD = D + 4;
     extern __shared__ float4 sm4[];
     float* sk = reinterpret_cast<float*>(sm4);   // [64][LD]
-    float* sq = sk + S_KEYS * LD;                // [32][LD]
+    float* sq = sk + S_KEYS * LD;                // [S_ROWS][LD]
     __shared__ float s_lse[S_ROWS];
     __shared__ int s_pos[S_ROWS];
     const int tid = threadIdx.x, kp = tid >> 2, qt = tid & 3;
@@ -66,24 +66,24 @@ __global__ void __launch_bounds__(128) accum_f32_kernel(AccumArgs a) {
             s_pos[tid] = f < end ? base + f / a.heads : -1;
         }
         __syncthreads();
-        float s[2][8];
+        float s[2][PP];
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[r][i] = 0.f;
+            for (int i = 0; i < PP; ++i) s[r][i] = 0.f;
 #pragma unroll 4
         for (int c = 0; c < D / 4; ++c) {
             const float4 x0 = *reinterpret_cast<const float4*>(sk + (2 * kp) * LD + 4 * c);
             const float4 x1 = *reinterpret_cast<const float4*>(sk + (2 * kp + 1) * LD + 4 * c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < PP; ++i) {
                 const float4 y = *reinterpret_cast<const float4*>(sq + (qt + 4 * i) * LD + 4 * c);
                 s[0][i] = fmaf(x0.x, y.x, fmaf(x0.y, y.y, fmaf(x0.z, y.z, fmaf(x0.w, y.w, s[0][i]))));
                 s[1][i] = fmaf(x1.x, y.x, fmaf(x1.y, y.y, fmaf(x1.z, y.z, fmaf(x1.w, y.w, s[1][i]))));
             }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < PP; ++i) {
             const int p = s_pos[qt + 4 * i];
             const float off = s_lse[qt + 4 * i];
 #pragma unroll
@@ -116,28 +116,37 @@ __global__ void __launch_bounds__(256) accum_join_kernel(AccumArgs a, int blocks
     a.acc_out[at] = a.acc_in ? fmaf(a.decay, a.acc_in[at], t) : t;
 }
 
-template <int D>
+template <int D, int PP>
 cudaError_t launch_f32(const AccumArgs& a, cudaStream_t st) {
-    constexpr int smem = (S_KEYS + S_ROWS) * (D + 4) * 4;
-    const cudaError_t e = cudaFuncSetAttribute(accum_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    constexpr int smem = (S_KEYS + 4 * PP) * (D + 4) * 4;
+    const cudaError_t e = cudaFuncSetAttribute(accum_f32_kernel<D, PP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const unsigned tiles = static_cast<unsigned>((a.max_ctx + S_KEYS - 1) / S_KEYS);
-    accum_f32_kernel<D><<<dim3(tiles * a.batch, a.splits), 128, smem, st>>>(a);
+    accum_f32_kernel<D, PP><<<dim3(tiles * a.batch, a.splits), 128, smem, st>>>(a);
     return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_f32(const AccumArgs& a, cudaStream_t st) {
+    return static_cast<int64_t>(a.n_q) * a.heads <= 16 ? launch_f32<D, 4>(a, st) : launch_f32<D, 8>(a, st);
 }
 
 }  // namespace
 
 int plan_accum(int batch, int n_q, int heads, int kv_dtype, int64_t max_ctx) {
     const bool f32 = kv_dtype == HS2_F32;
-    const int64_t keys = f32 ? S_KEYS : 256, rows = f32 ? S_ROWS : 128;
-    const int64_t blocks = (max_ctx + keys - 1) / keys * batch;
+    const int64_t keys = f32 ? S_KEYS : 256, rows = f32 ? 32 : 128;
+    const int64_t blocks = (max_ctx + keys - 1) / keys * batch, slots = (f32 ? 3 : 1) * num_sms();
     const int64_t tiles = (static_cast<int64_t>(n_q) * heads + rows - 1) / rows;
-    // parts of the pairs: where key blocks alone leave SMs idle, each with a few tiles of pairs
-    int64_t s = (f32 ? 3 : 1) * num_sms() / blocks;
-    const int64_t most = tiles / (f32 ? 4 : 2);
-    if (s > most) s = most;
-    return s < 1 ? 1 : static_cast<int>(s);
+    // Parts of the pairs: the number that leaves the fewest idle SMs in the last round of key
+    // blocks, each part with a few tiles of pairs; a part more has to save 1% (300 rows over 50000
+    // bf16 keys, 196 blocks on 148 SMs: 118 us in one part, 84 in three).
+    int best = 1;
+    int64_t cost = -1;
+    for (int64_t s = 1; s <= 64 && s * (f32 ? 4 : 2) <= (tiles > 1 ? tiles : 1) + (s == 1 ? 4 : 0); ++s) {
+        const int64_t rounds = (blocks * s + slots - 1) / slots, c = rounds * 1000 / s + 10 * s;
+        if (cost < 0 || c < cost) { cost = c; best = static_cast<int>(s); }
+    }
+    return best;
 }
 
 size_t accum_part_bytes(int batch, int splits, int64_t max_ctx) {
