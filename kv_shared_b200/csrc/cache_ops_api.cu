@@ -16,6 +16,15 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
+struct Extent {
+    const void* p;
+    int64_t bytes;
+};
+bool overlap(const Extent& x, const Extent& y) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    return x.p && y.p && (a <= b ? b - a < static_cast<uintptr_t>(x.bytes) : a - b < static_cast<uintptr_t>(y.bytes));
+}
+
 hs2_status from_cuda(cudaError_t e) { return e == cudaSuccess ? HS2_OK : HS2_ERR_CUDA; }
 
 // The fields that hs2_window_attn and hs2_weight_accum use.
@@ -183,6 +192,18 @@ hs2_status hs2_kv_evict(const hs2_evict_desc* desc, const int32_t* len, const fl
     const void* p4[] = {len, acc, acc_out, idx, new_len, k_scale, v_scale, k_scale_out, v_scale_out};
     for (const void* p : p4)
         if (!aligned4(p)) return HS2_ERR_INVALID_ARG;
+    // the rows move in no order, so that a cache cannot be cut in place
+    const bool e4 = d.kv_dtype == HS2_E4M3;
+    const int64_t row = static_cast<int64_t>(d.head_dim) * (e4 ? 1 : d.kv_dtype == HS2_BF16 ? 2 : 4);
+    const int64_t n_in = d.batch * d.kv_capacity, n_out = d.batch * d.out_capacity;
+    const Extent in[] = {{k, n_in * row}, {v, n_in * row}, {acc, n_in * 4},
+                         {e4 ? k_scale : nullptr, n_in * 4}, {e4 ? v_scale : nullptr, n_in * 4}};
+    const Extent out[] = {{k_out, n_out * row}, {v_out, n_out * row}, {acc_out, n_out * 4},
+                          {e4 ? k_scale_out : nullptr, n_out * 4}, {e4 ? v_scale_out : nullptr, n_out * 4},
+                          {idx, d.batch * keep * 4}};
+    for (const Extent& x : in)
+        for (const Extent& y : out)
+            if (overlap(x, y)) return HS2_ERR_INVALID_ARG;
     EvictArgs a{};
     a.batch = d.batch; a.head_dim = d.head_dim; a.kv_dtype = d.kv_dtype;
     a.sinks = d.sinks; a.window = d.window; a.budget = d.budget; a.cap = d.kv_capacity; a.out_cap = d.out_capacity;

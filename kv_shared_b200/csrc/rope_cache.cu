@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(NT) rope_cache_kernel(RopeArgs a, int wpr, int
     if (is_k) load8(kv, static_cast<const T*>(a.k) + row * a.k_row, d0, d1, TOGETHER);
     if (is_v) load8(kv, static_cast<const T*>(a.v) + row * a.v_row, d0, d1, TOGETHER);
     {
-        const int p = a.pos ? a.pos[row] : static_cast<int>(at);
+        const double p = a.pos ? a.pos[row] : static_cast<double>(at);
         for (int j = lane; j < half; j += 32) {
             const double turns = p * (a.inv_freq[j] * 0.15915494309189533577);  // 1 / (2 pi)
             float s, c;

@@ -149,6 +149,22 @@ def test_evict_refuses(L, desc, args, status):
     assert _evict(L, hs.make_evict_desc(**base), **args) == status
 
 
+@pytest.mark.parametrize("kv", [hs.HS2_BF16, hs.HS2_E4M3])
+@pytest.mark.parametrize("out, at", [("ko", "k"), ("vo", "v"), ("acco", "acc"), ("idx", "acc"), ("ko", "acc"), ("vo", "k")])
+def test_evict_refuses_a_cache_cut_in_place(L, kv, out, at):
+    """Outputs that start at an input, inside it, or reach into it."""
+    names = ("len", "acc", "k", "v", "ks", "vs", "ko", "vo", "kso", "vso", "acco", "idx", "new_len")
+    where = {n: (i + 1) << 32 for i, n in enumerate(names)}
+    d = hs.make_evict_desc(2, 128, kv, 4, 128, 1024, 4096, 2000)
+    for off in (0, 64, 2 * 4096 * 4 - 16, -16):
+        args = {n: ctypes.c_void_p(x) for n, x in where.items()}
+        args[out] = ctypes.c_void_p(where[at] + off)
+        assert _evict(L, d, **args) == 1
+    if kv == hs.HS2_E4M3:
+        args = {n: ctypes.c_void_p(x) for n, x in where.items()}
+        assert _evict(L, d, **dict(args, kso=args["ks"])) == _evict(L, d, **dict(args, vso=args["vs"])) == 1
+
+
 # ---------------------------------------------------------------- the fp64 forms
 def test_rotation_keeps_lengths_and_relative_angles():
     g = torch.Generator().manual_seed(1)

@@ -26,6 +26,24 @@ def test_rope_a_warp_to_a_row(b, n, h, d, rot, inter, dt, kv):
     base.test_rope_rows(b, n, h, d, rot, inter, dt, kv, True)
 
 
+def test_rope_positions_follow_rows_past_32_bits():
+    """Without positions the position is the cache row, also where the rows lie behind any cache: the
+    queries turn by it, the key is not written."""
+    n, h, d = 6, 3, 64
+    g = base._gen(31)
+    q0, k0 = torch.randn(1, n, h, d, generator=g), torch.randn(1, n, d, generator=g)
+    freq = 1e4 ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)
+    row0 = torch.tensor([(1 << 31) - 3], dtype=torch.int32)
+    q, k, fr, r0 = base._cu(q0, k0, freq, row0)
+    out, kc = torch.empty_like(q), torch.full((1, 8, d), 7.0, device="cuda")
+    desc = hs.make_rope_desc(1, n, h, d, normalize=False, in_dtype=hs.HS2_F32, kv_dtype=hs.HS2_F32, kv_capacity=8)
+    hs.hs2_qk_norm_rope(desc, q, k, None, None, None, fr, r0, None, None, out, kc, None)
+    torch.cuda.synchronize()
+    want = ref.norm_rope(q0[0], None, 0.0, [int(row0[0]) + t for t in range(n)], freq, False, normalize=False)
+    assert (out[0].cpu().double() - want).abs().le(2.0 ** -18 * want.abs().amax(-1, keepdim=True)).all()
+    assert (kc == 7).all()
+
+
 # ------------------------------------------------------------------ sliding window
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("b, n, h, d, window, sinks, ctx", [
