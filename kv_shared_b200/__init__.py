@@ -2,7 +2,8 @@
 
 Argument marshalling only: every function below forwards torch tensors (device
 memory) and the current CUDA stream to the C ABI declared in include/hs2.h, with
-the same names, and raises HS2Error on a non-OK status.  All computation runs in
+the same names, and raises HS2Error on a non-OK status (through ctypes; the calls
+around the block, some of which run for a few microseconds, through csrc/calls.c).  All computation runs in
 the CUDA kernels of libhs2.so; there is no fallback.  Build the library with
 ``python -m kv_shared_b200.build`` (or ``__graft_entry__.build()``).
 """
@@ -91,8 +92,25 @@ def lib():
     return _lib
 
 
-# Addresses go over as plain integers (the argument types make pointers of them): a call of
-# ten tensors spends less time here than its kernel runs.
+_bound = None
+
+
+def _fast():
+    """The calls around the block as functions that take tensors (csrc/calls.c); raises if it has not been built."""
+    global _bound
+    if _bound is None:
+        L = lib()
+        try:
+            from kv_shared_b200 import _calls as m
+        except ImportError as e:
+            raise RuntimeError("kv_shared_b200/_calls.so is missing: build it with `python -m kv_shared_b200.build`") from e
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                 for f in (L.hs2_qk_norm_rope, L.hs2_window_attn, L.hs2_weight_accum, L.hs2_kv_evict)))
+        _bound = m
+    return _bound
+
+
+# Addresses go over as plain integers (the argument types make pointers of them).
 def _p(t):
     return None if t is None else t.data_ptr()
 
@@ -208,9 +226,8 @@ def make_evict_desc(batch, head_dim, kv_dtype=HS2_BF16, sinks=0, window=128, bud
 
 def hs2_qk_norm_rope(desc, q, k, v, q_weight, k_weight, inv_freq, row0, pos, n_rows, q_out, k_cache, v_cache,
                      k_scale=None, v_scale=None, stream=None):
-    st = lib().hs2_qk_norm_rope(ctypes.byref(desc), _p(q), _p(k), _p(v), _p(q_weight), _p(k_weight), _p(inv_freq),
-                                _p(row0), _p(pos), _p(n_rows), _p(q_out), _p(k_cache), _p(v_cache), _p(k_scale),
-                                _p(v_scale), _stream(stream))
+    st = _fast().qk_norm_rope(desc, q, k, v, q_weight, k_weight, inv_freq, row0, pos, n_rows, q_out, k_cache, v_cache,
+                              k_scale, v_scale, _stream(stream))
     _check("hs2_qk_norm_rope", st)
 
 
@@ -219,9 +236,8 @@ def hs2_window_workspace_size(desc, sinks=0):
 
 
 def hs2_window_attn(desc, sinks, q, k, v, k_scale, v_scale, q_pos0, n_rows, o, lse, workspace, stream=None):
-    st = lib().hs2_window_attn(ctypes.byref(desc), int(sinks), _p(q), _p(k), _p(v), _p(k_scale), _p(v_scale),
-                               _p(q_pos0), _p(n_rows), _p(o), _p(lse), _p(workspace),
-                               workspace.numel() * workspace.element_size(), _stream(stream))
+    st = _fast().window_attn(desc, int(sinks), q, k, v, k_scale, v_scale, q_pos0, n_rows, o, lse, workspace,
+                             workspace.numel() * workspace.element_size(), _stream(stream))
     _check("hs2_window_attn", st)
 
 
@@ -230,17 +246,15 @@ def hs2_weight_accum_workspace_size(desc):
 
 
 def hs2_weight_accum(desc, q, k, k_scale, lse, q_pos0, n_rows, decay, acc_in, acc_out, workspace, stream=None):
-    st = lib().hs2_weight_accum(ctypes.byref(desc), _p(q), _p(k), _p(k_scale), _p(lse), _p(q_pos0), _p(n_rows),
-                                float(decay), _p(acc_in), _p(acc_out), _p(workspace),
-                                workspace.numel() * workspace.element_size(), _stream(stream))
+    st = _fast().weight_accum(desc, q, k, k_scale, lse, q_pos0, n_rows, decay, acc_in, acc_out, workspace,
+                              workspace.numel() * workspace.element_size(), _stream(stream))
     _check("hs2_weight_accum", st)
 
 
 def hs2_kv_evict(desc, len_, acc, k, v, k_scale, v_scale, k_out, v_out, k_scale_out, v_scale_out, acc_out, idx,
                  new_len, stream=None):
-    st = lib().hs2_kv_evict(ctypes.byref(desc), _p(len_), _p(acc), _p(k), _p(v), _p(k_scale), _p(v_scale), _p(k_out),
-                            _p(v_out), _p(k_scale_out), _p(v_scale_out), _p(acc_out), _p(idx), _p(new_len),
-                            _stream(stream))
+    st = _fast().kv_evict(desc, len_, acc, k, v, k_scale, v_scale, k_out, v_out, k_scale_out, v_scale_out, acc_out, idx,
+                          new_len, _stream(stream))
     _check("hs2_kv_evict", st)
 
 

@@ -2,19 +2,22 @@
 
 Each csrc/*.cu file is compiled to an object (in parallel) and linked into
 kv_shared_b200/libhs2.so with the CUDA runtime linked statically, so the
-library carries no dependency on the runtime version torch ships.
+library carries no dependency on the runtime version torch ships.  csrc/calls.c,
+the binding's fast calls, becomes kv_shared_b200/_calls.so with the host compiler.
 """
 import concurrent.futures as cf
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhs2.so")
+CALLS_SRC, CALLS = os.path.join(CSRC, "calls.c"), os.path.join(HERE, "_calls.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -45,11 +48,24 @@ def _compile(src, verbose=False):
     return obj
 
 
+def _build_calls(force=False):
+    deps = [CALLS_SRC, os.path.join(ROOT, "include", "hs2.h")]
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= max(map(os.path.getmtime, deps)):
+        return
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-fvisibility=hidden",
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(ROOT, "include"), CALLS_SRC, "-o", CALLS + ".tmp"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(CALLS + ".tmp", CALLS)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OBJ, exist_ok=True)
     if force:
         for o in glob.glob(os.path.join(OBJ, "*.o")):
             os.remove(o)
+    _build_calls(force)
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
