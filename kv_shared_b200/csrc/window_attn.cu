@@ -18,6 +18,7 @@
 // well and a second launch joins the parts in a fixed order.  Measured (16 heads of 128): 32
 // tokens, window 128: 5.7 us; 4 tokens, window 32768, e4m3: 15.1 us (2.3 TB/s).
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "internal.h"
 #include "tile_sync.cuh"
 #include "window_keys.cuh"
@@ -29,10 +30,10 @@ constexpr int NW = 8;                            // warps per CTA
 constexpr int STEP = 16;                         // keys per warp step
 constexpr float kLag = 4.f;                      // log2 units: weights stay below 2^4, f16's products far from its end
 constexpr int kMinSplitKeys = 512;               // keys per CTA below which a split costs more than it saves
-constexpr int F_QT = 8;                          // fp32: threads that share two pairs
-constexpr int F_ROWS = 2 * 128 / F_QT;           // (row, head) pairs per CTA
+constexpr int F_QT = 8;                          // fp32: threads that share a few pairs
+constexpr int F_ROWS = 32;                       // (row, head) pairs per CTA
 constexpr int F_KEYS = 32;                       // keys per tile
-constexpr int kMinSplitKeysF32 = 256;
+constexpr int kMinSplitKeysF32 = 32;
 constexpr int kMinSplitKeysTile = 256;
 
 template <int D, bool KV8>
@@ -379,11 +380,15 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a, F
 }
 
 // fp32: 32 pairs x 32 keys per tile on the CUDA cores (a bf16 or tf32 product would lose what
-// the fp32 caches are there for).  Thread (rp, qt) of 16 x 8 has pairs 2 rp, 2 rp + 1; keys
-// qt + 8 i of S, dims 4 (qt + 8 j) of O.  Bound by the shared-memory loads between the FMAs (10
-// of 16 bytes to 64 FMAs): 2 x 1023 rows of 8 heads of 64, window 128, 31 us.
-template <int D>
-__global__ void __launch_bounds__(128) window_f32_kernel(WindowArgs a) {
+// the fp32 caches are there for).  Thread (rp, qt) of 32 / RP x 8 has pairs RP rp .. RP rp + RP - 1;
+// keys qt + 8 i of S, dims 4 (qt + 8 j) of O, two fp32 FMAs to an instruction.  RP = 4 makes 8 loads
+// of 16 bytes from shared memory to 64 FMAs and is bound by them and by latency: 2 x 1023 rows of 8
+// heads of 64, window 128, 26.0 us (RP = 2, 12 to 64: 31.4).  RP = 2 has twice the warps, for calls
+// that leave each SM a CTA at most and are bound by a tile's latency alone, some 2 us: one row of 16
+// heads of 128, window 4096, 14.0 us (RP = 4: 18.5; parts of 256 keys and not of one tile: 37.7).
+template <int D, int RP>
+__global__ void __launch_bounds__(F_ROWS / RP * F_QT) window_f32_kernel(WindowArgs a) {
+    constexpr int NT = F_ROWS / RP * F_QT;
     constexpr int LDQ = D + 4;                   // row pitch: rows of a quarter-warp on distinct banks
     constexpr int LDP = F_KEYS + 4;
     constexpr int NC = D / (4 * F_QT);           // float4 chunks of O per thread and pair
@@ -406,19 +411,21 @@ __global__ void __launch_bounds__(128) window_f32_kernel(WindowArgs a) {
     const int64_t flat0 = static_cast<int64_t>(b) * a.n_q * a.heads;
     const float sc2 = a.scale * kLog2e;
 
-    for (int i = tid; i < F_ROWS * D / 4; i += 128) {
+    for (int i = tid; i < F_ROWS * D / 4; i += NT) {
         const int r = i / (D / 4), c = i - r * (D / 4);
         const float4 x = f0 + r <= f_last ? __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (flat0 + f0 + r) * D) + c)
                                           : make_float4(0.f, 0.f, 0.f, 0.f);
         *reinterpret_cast<float4*>(sq + r * LDQ + 4 * c) = x;
     }
-    int pos[2];
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float4 o[2][NC];
+    int pos[RP];
+    float m[RP], l[RP];
+    float4 o[RP][NC];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int f = f0 + 2 * rp + r;
+    for (int r = 0; r < RP; ++r) {
+        const int f = f0 + RP * rp + r;
         pos[r] = f <= f_last ? base + f / a.heads : -1;
+        m[r] = -INFINITY;
+        l[r] = 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -426,7 +433,7 @@ __global__ void __launch_bounds__(128) window_f32_kernel(WindowArgs a) {
         float* sk = kv + buf * F_KEYS * (LDQ + D);
         float* sv = sk + F_KEYS * LDQ;
 #pragma unroll
-        for (int i = tid; i < F_KEYS * D / 4; i += 128) {
+        for (int i = tid; i < F_KEYS * D / 4; i += NT) {
             const int r = i / (D / 4), c = i - r * (D / 4);
             const int key = u0 + r < end ? kl.row(u0 + r) : -1;
             const int64_t src = (seq0 + max(key, 0)) * D + 4 * c;
@@ -444,30 +451,42 @@ __global__ void __launch_bounds__(128) window_f32_kernel(WindowArgs a) {
         __syncthreads();
         const float* sk = kv + buf * F_KEYS * (LDQ + D);
         const float* sv = sk + F_KEYS * LDQ;
-        float s[2][KPT];
+        float2 d[RP][KPT];                     // sums over the even and the odd dims
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < RP; ++r)
 #pragma unroll
-            for (int i = 0; i < KPT; ++i) s[r][i] = 0.f;
-#pragma unroll 8
+            for (int i = 0; i < KPT; ++i) d[r][i] = make_float2(0.f, 0.f);
+#pragma unroll (RP == 2 ? 8 : 4)
         for (int c = 0; c < D / 4; ++c) {
-            const float4 x0 = *reinterpret_cast<const float4*>(sq + (2 * rp) * LDQ + 4 * c);
-            const float4 x1 = *reinterpret_cast<const float4*>(sq + (2 * rp + 1) * LDQ + 4 * c);
+            float4 x[RP];
+#pragma unroll
+            for (int r = 0; r < RP; ++r) x[r] = *reinterpret_cast<const float4*>(sq + (RP * rp + r) * LDQ + 4 * c);
 #pragma unroll
             for (int i = 0; i < KPT; ++i) {
                 const float4 y = *reinterpret_cast<const float4*>(sk + (qt + F_QT * i) * LDQ + 4 * c);
-                s[0][i] = fmaf(x0.x, y.x, fmaf(x0.y, y.y, fmaf(x0.z, y.z, fmaf(x0.w, y.w, s[0][i]))));
-                s[1][i] = fmaf(x1.x, y.x, fmaf(x1.y, y.y, fmaf(x1.z, y.z, fmaf(x1.w, y.w, s[1][i]))));
+#pragma unroll
+                for (int r = 0; r < RP; ++r)
+                    d[r][i] = fma2(make_float2(x[r].x, x[r].y), make_float2(y.x, y.y),
+                                   fma2(make_float2(x[r].z, x[r].w), make_float2(y.z, y.w), d[r][i]));
             }
         }
+        float s[RP][KPT];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < RP; ++r)
+#pragma unroll
+            for (int i = 0; i < KPT; ++i) s[r][i] = d[r][i].x + d[r][i].y;
+        int key[KPT];
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            const int u = u0 + qt + F_QT * i;
+            key[i] = u < end ? kl.row(u) : -1;
+        }
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
             float mx = -INFINITY;
 #pragma unroll
             for (int i = 0; i < KPT; ++i) {
-                const int u = u0 + qt + F_QT * i;
-                const int key = u < end ? kl.row(u) : -1;
-                s[r][i] = window_sees(key, pos[r], a.window, a.sinks) ? s[r][i] * sc2 : -INFINITY;
+                s[r][i] = window_sees(key[i], pos[r], a.window, a.sinks) ? s[r][i] * sc2 : -INFINITY;
                 mx = fmaxf(mx, s[r][i]);
             }
 #pragma unroll
@@ -479,7 +498,7 @@ __global__ void __launch_bounds__(128) window_f32_kernel(WindowArgs a) {
             for (int i = 0; i < KPT; ++i) {
                 const float p = exp2f(s[r][i] - off);
                 sum += p;
-                sp[(2 * rp + r) * LDP + qt + F_QT * i] = p;
+                sp[(RP * rp + r) * LDP + qt + F_QT * i] = p;
             }
             l[r] = fmaf(l[r], c, sum);
             m[r] = mn;
@@ -489,27 +508,30 @@ __global__ void __launch_bounds__(128) window_f32_kernel(WindowArgs a) {
         __syncwarp();                            // a pair's weights come from its F_QT neighbouring threads
 #pragma unroll 4
         for (int k = 0; k < F_KEYS; k += 4) {
-            const float4 w0 = *reinterpret_cast<const float4*>(sp + (2 * rp) * LDP + k);
-            const float4 w1 = *reinterpret_cast<const float4*>(sp + (2 * rp + 1) * LDP + k);
-            const float p0[4] = {w0.x, w0.y, w0.z, w0.w}, p1[4] = {w1.x, w1.y, w1.z, w1.w};
+            float4 w[RP];
+#pragma unroll
+            for (int r = 0; r < RP; ++r) w[r] = *reinterpret_cast<const float4*>(sp + (RP * rp + r) * LDP + k);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < NC; ++j) {
                     const float4 y = *reinterpret_cast<const float4*>(sv + (k + i) * D + 4 * (qt + F_QT * j));
-                    o[0][j].x = fmaf(p0[i], y.x, o[0][j].x); o[0][j].y = fmaf(p0[i], y.y, o[0][j].y);
-                    o[0][j].z = fmaf(p0[i], y.z, o[0][j].z); o[0][j].w = fmaf(p0[i], y.w, o[0][j].w);
-                    o[1][j].x = fmaf(p1[i], y.x, o[1][j].x); o[1][j].y = fmaf(p1[i], y.y, o[1][j].y);
-                    o[1][j].z = fmaf(p1[i], y.z, o[1][j].z); o[1][j].w = fmaf(p1[i], y.w, o[1][j].w);
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) {
+                        const float p = i == 0 ? w[r].x : i == 1 ? w[r].y : i == 2 ? w[r].z : w[r].w;
+                        const float2 lo = fma2(make_float2(p, p), make_float2(y.x, y.y), make_float2(o[r][j].x, o[r][j].y));
+                        const float2 hi = fma2(make_float2(p, p), make_float2(y.z, y.w), make_float2(o[r][j].z, o[r][j].w));
+                        o[r][j] = make_float4(lo.x, lo.y, hi.x, hi.y);
+                    }
                 }
         }
         __syncthreads();                         // the tile may be overwritten
     }
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < RP; ++r) {
 #pragma unroll
         for (int o1 = 1; o1 < F_QT; o1 <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o1);
-        const int f = f0 + 2 * rp + r;
+        const int f = f0 + RP * rp + r;
         if (f > f_last) continue;
         const int64_t flat = flat0 + f;
         const int64_t at = static_cast<int64_t>(blockIdx.y) * a.batch * a.n_q * a.heads + flat;
@@ -598,14 +620,19 @@ cudaError_t launch_rows(const WindowArgs& a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+template <int D, int RP>
+cudaError_t launch_f32(const WindowArgs& a, unsigned tiles, cudaStream_t st) {
+    constexpr int smem = (F_ROWS * (D + 4) + F_ROWS * (F_KEYS + 4) + 2 * F_KEYS * (2 * D + 4)) * 4;
+    const cudaError_t e = cudaFuncSetAttribute(window_f32_kernel<D, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    window_f32_kernel<D, RP><<<dim3(tiles * a.batch, a.splits), F_ROWS / RP * F_QT, smem, st>>>(a);
+    return cudaGetLastError();
+}
 template <int D>
 cudaError_t launch_f32(const WindowArgs& a, cudaStream_t st) {
-    constexpr int smem = (F_ROWS * (D + 4) + F_ROWS * (F_KEYS + 4) + 2 * F_KEYS * (2 * D + 4)) * 4;
-    const cudaError_t e = cudaFuncSetAttribute(window_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
     const unsigned tiles = (static_cast<unsigned>(a.n_q) * a.heads + F_ROWS - 1) / F_ROWS;
-    window_f32_kernel<D><<<dim3(tiles * a.batch, a.splits), 128, smem, st>>>(a);
-    return cudaGetLastError();
+    return static_cast<int64_t>(tiles) * a.batch * a.splits > num_sms() ? launch_f32<D, 4>(a, tiles, st)
+                                                                        : launch_f32<D, 2>(a, tiles, st);
 }
 
 template <typename T, int D>

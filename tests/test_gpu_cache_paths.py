@@ -76,6 +76,16 @@ def test_window_large_calls(kv, b, n, h, d, window, sinks, ctx):
     base._run_window(base._gen(n + ctx), b, n, h, d, window, sinks, ctx, kv, ragged=b == 4, rows=rows)
 
 
+@pytest.mark.parametrize("b, n, h, d, window, sinks, ctx", [
+    (2, 700, 8, 64, 100, 4, 900), (1, 340, 16, 128, 2000, 5, 3000),        # a CTA and more on every SM
+    (1, 90, 16, 128, 1500, 40, 2000), (4, 30, 8, 64, 31, 33, 200),         # keys cut over the CTAs; a padded batch
+    (1, 1, 3, 64, 4000, 0, 5000), (1, 7, 1, 128, 64, 1, 64),               # parts of a tile of keys each
+])
+def test_window_f32_calls(b, n, h, d, window, sinks, ctx):
+    rows = sorted({0, 1, 2, 3, 4, 31, 32, n // 2, max(n - 2, 0), n - 1})
+    base._run_window(base._gen(n + ctx), b, n, h, d, window, sinks, ctx, "f32", ragged=b == 4, rows=rows)
+
+
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_window_large_call_with_rising_logits(kv):
     """Logits of several hundred that rise along the keys, so that the reference moves at every tile."""
