@@ -1,8 +1,8 @@
 /* calls.c -- Python's way into the four calls around the block, argument marshalling only.
  *
  * A single token's call is a few microseconds on the device, and forming its sixteen arguments
- * through ctypes took 3.0 us of the host's time, half of what the whole call took; here it is
- * under one.  The library's functions are handed over as addresses once it is loaded, so that
+ * through ctypes took 3.0 us of the host's time, half of what the whole call took; here it
+ * takes 1.0.  The library's functions are handed over as addresses once it is loaded, so that
  * this module links against nothing.
  */
 #define PY_SSIZE_T_CLEAN
