@@ -192,18 +192,20 @@ hs2_status hs2_kv_evict(const hs2_evict_desc* desc, const int32_t* len, const fl
     const void* p4[] = {len, acc, acc_out, idx, new_len, k_scale, v_scale, k_scale_out, v_scale_out};
     for (const void* p : p4)
         if (!aligned4(p)) return HS2_ERR_INVALID_ARG;
-    // the rows move in no order, so that a cache cannot be cut in place
+    // the rows move in no order, so that a cache cannot be cut in place; the new lengths are written
+    // when the lengths have been read and may take their place
     const bool e4 = d.kv_dtype == HS2_E4M3;
     const int64_t row = static_cast<int64_t>(d.head_dim) * (e4 ? 1 : d.kv_dtype == HS2_BF16 ? 2 : 4);
     const int64_t n_in = d.batch * d.kv_capacity, n_out = d.batch * d.out_capacity;
-    const Extent in[] = {{k, n_in * row}, {v, n_in * row}, {acc, n_in * 4},
+    const int64_t n_seq = static_cast<int64_t>(d.batch) * 4;
+    const Extent in[] = {{len, n_seq}, {k, n_in * row}, {v, n_in * row}, {acc, n_in * 4},
                          {e4 ? k_scale : nullptr, n_in * 4}, {e4 ? v_scale : nullptr, n_in * 4}};
-    const Extent out[] = {{k_out, n_out * row}, {v_out, n_out * row}, {acc_out, n_out * 4},
+    const Extent out[] = {{new_len, n_seq}, {k_out, n_out * row}, {v_out, n_out * row}, {acc_out, n_out * 4},
                           {e4 ? k_scale_out : nullptr, n_out * 4}, {e4 ? v_scale_out : nullptr, n_out * 4},
                           {idx, d.batch * keep * 4}};
     for (const Extent& x : in)
         for (const Extent& y : out)
-            if (overlap(x, y)) return HS2_ERR_INVALID_ARG;
+            if (overlap(x, y) && !(&x == in && &y == out && len == new_len)) return HS2_ERR_INVALID_ARG;
     EvictArgs a{};
     a.batch = d.batch; a.head_dim = d.head_dim; a.kv_dtype = d.kv_dtype;
     a.sinks = d.sinks; a.window = d.window; a.budget = d.budget; a.cap = d.kv_capacity; a.out_cap = d.out_capacity;

@@ -15,7 +15,9 @@
 //           overwrites).  The patterns stay in shared memory; slices too long for it (many
 //           sequences, each over 40960 rows a CTA) are read again, and only the rows that share
 //           the first digit are listed.
-//   move    one warp per few rows copies K, V, scales and totals to their new places.
+//   move    one warp per few rows copies K, V, scales and totals to their new places, and one thread
+//           per sequence writes the new length: every CTA of the selection has read the old one by
+//           then, so that lengths may be cut in place.
 //
 // The move is bound by HBM (twice the surviving rows' bytes: 525,000 e4m3 rows 50 us, 32 x 4228
 // bf16 rows 24.6 us), the selection by its barriers (5 to 9 us for one CTA, 22 us for 1M rows or 32 x 64K).
@@ -100,7 +102,6 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(EvictArgs a) {
     const int n = static_cast<int>(n64);
     const int kept = n < keep ? n : static_cast<int>(keep);
     int32_t* idx = a.idx + b * keep;
-    if (cr == 0 && tid == 0) a.new_len[b] = kept;
     for (int64_t i = kept + cr * ST + tid; i < keep; i += cs * ST) idx[i] = -1;
     if (n <= keep) {                                            // the whole cluster takes this branch
         for (int i = cr * ST + tid; i < n; i += cs * ST) idx[i] = i;
@@ -321,7 +322,6 @@ __global__ void __launch_bounds__(ST) evict_team_kernel(EvictArgs a, int team, i
             }
     }
     // what does not depend on the totals
-    if (tr == 0 && tid == 0) a.new_len[b] = kept;
     for (int64_t i = kept + tr * ST + tid; i < keep; i += team * ST) idx[i] = -1;
     if (n <= keep) {
         for (int i = tr * ST + tid; i < n; i += team * ST) idx[i] = i;
@@ -456,6 +456,10 @@ __global__ void __launch_bounds__(256) evict_move_kernel(EvictArgs a, int64_t ke
     const int lane = threadIdx.x & 31;
     const int64_t w = static_cast<int64_t>(blockIdx.x - b * blocks) * 8 + (threadIdx.x >> 5);
     const int64_t r0 = w * RPS * UN;
+    if (w == 0 && lane == 0) {
+        const int64_t n = min(max(static_cast<int64_t>(a.len[b]), int64_t(0)), a.cap);
+        a.new_len[b] = static_cast<int32_t>(min(n, keep));
+    }
     const int32_t* idx = a.idx + b * keep;
     const uint4* k = static_cast<const uint4*>(a.k) + b * a.cap * LPR;
     const uint4* v = static_cast<const uint4*>(a.v) + b * a.cap * LPR;
