@@ -387,8 +387,8 @@ typedef struct {
  * ascending, then -1.  Output rows from new_len[b] on are left as they were.
  *   len      device int32 [batch], clamped to [0, kv_capacity]
  *   acc      [batch][kv_capacity] fp32; acc_out optional [batch][out_capacity]
- * new_len may be len itself; any other output that overlaps an input is refused
- * (HS2_ERR_INVALID_ARG).  No workspace.
+ * new_len may be len itself; any other output that overlaps an input or another output
+ * is refused (HS2_ERR_INVALID_ARG).  No workspace.
  */
 HS2_API hs2_status hs2_kv_evict(const hs2_evict_desc* desc, const int32_t* len, const float* acc, const void* k,
                                 const void* v, const float* k_scale, const float* v_scale, void* k_out,

@@ -206,6 +206,10 @@ hs2_status hs2_kv_evict(const hs2_evict_desc* desc, const int32_t* len, const fl
     for (const Extent& x : in)
         for (const Extent& y : out)
             if (overlap(x, y) && !(&x == in && &y == out && len == new_len)) return HS2_ERR_INVALID_ARG;
+    // nor may outputs meet: k_out holds counts that the kept rows' places follow from
+    for (const Extent& x : out)
+        for (const Extent& y : out)
+            if (&x < &y && overlap(x, y)) return HS2_ERR_INVALID_ARG;
     EvictArgs a{};
     a.batch = d.batch; a.head_dim = d.head_dim; a.kv_dtype = d.kv_dtype;
     a.sinks = d.sinks; a.window = d.window; a.budget = d.budget; a.cap = d.kv_capacity; a.out_cap = d.out_capacity;

@@ -61,3 +61,17 @@ def test_evict_takes_buffers_that_touch(L):
     assert _evict(L, new_len=WHERE["len"] + BATCH * 4) != hs.HS2_ERR_INVALID_ARG
     assert _evict(L, idx=WHERE["len"] + BATCH * 4) != hs.HS2_ERR_INVALID_ARG
     assert _evict(L, idx=WHERE["len"] - BATCH * KEEP * 4) != hs.HS2_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kv", [hs.HS2_BF16, hs.HS2_E4M3])
+def test_evict_refuses_outputs_over_one_another(L, kv):
+    """k_out holds the selection's counts before its rows: an index or a length written there, or any
+    output twice in one place, would be the call's own undoing."""
+    names = [n for n in OUTPUTS if kv == hs.HS2_E4M3 or n not in ("kso", "vso")]
+    for a in names:
+        for b in names:
+            if a != b:
+                for off in (0,) if b == "new_len" else (0, 16):
+                    assert _evict(L, kv, **{a: WHERE[b] + off}) == hs.HS2_ERR_INVALID_ARG, (a, b, off)
+    assert _evict(L, kv, idx=WHERE["ko"] + BATCH * OUT * 128 * (1 if kv == hs.HS2_E4M3 else 2)) != hs.HS2_ERR_INVALID_ARG
+    assert _evict(L, kv, new_len=WHERE["idx"] + BATCH * KEEP * 4) != hs.HS2_ERR_INVALID_ARG
