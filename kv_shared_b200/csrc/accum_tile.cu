@@ -478,7 +478,8 @@ cudaError_t launch(TileArgs& p, const CUtensorMap& km, const CUtensorMap& qm, cu
     p.k_stages = (free_bytes - p.q_slots * p.q_bytes) / Sh::KTILE;
     if (p.k_stages > 16) p.k_stages = 16;
     const int smem = OFF_TILES + p.q_slots * p.q_bytes + p.k_stages * Sh::KTILE;
-    const cudaError_t e = cudaFuncSetAttribute(accum_tile_kernel<D, KV8, NARROW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // The function's limit, the same in every call: another thread's call may set it before this launch.
+    const cudaError_t e = cudaFuncSetAttribute(accum_tile_kernel<D, KV8, NARROW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int64_t items = static_cast<int64_t>(p.walk.batch) * p.walk.tiles * p.walk.parts;
     const int grid = items < num_sms() ? static_cast<int>(items) : num_sms();

@@ -276,6 +276,7 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(EvictArgs a) {
 // cluster, or any number that meets in grid-wide barriers (GRID).
 constexpr int kKeys = 40960;                     // rows of a CTA's slice, at most
 constexpr int team_smem(int64_t slice) { return static_cast<int>((COPIES * BINS + BINS + slice) * 4); }
+constexpr int kTeamSmem = team_smem(kKeys);
 constexpr int kScratchInts = 3 * BINS;           // GRID: counts of the three rounds; then two per CTA
 enum { ONE = 0, CLUSTER = 1, GRID = 2 };
 
@@ -511,9 +512,12 @@ int cluster_size(const EvictArgs& a) {
     return cs;
 }
 
+// `most`: the largest smem that any call gives the kernel.  The limit belongs to the function in the
+// whole process, so every call sets the same one (a call's own size, set by another thread between this
+// thread's set and its launch, made the launch fail).
 template <typename Kernel, typename... Args>
-cudaError_t launch_select(Kernel kernel, int grid, int smem, cudaLaunchAttribute at, cudaStream_t st, Args... args) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+cudaError_t launch_select(Kernel kernel, int grid, int smem, int most, cudaLaunchAttribute at, cudaStream_t st, Args... args) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -534,7 +538,7 @@ cudaError_t select(const EvictArgs& a, int64_t keep, int row, cudaStream_t st) {
     coop.val.cooperative = 1;
     if (a.cap <= kOneRows) {
         cluster.val.clusterDim.x = 1;
-        return launch_select(evict_team_kernel<ONE>, a.batch, team_smem(a.cap), cluster, st, a, 1, row);
+        return launch_select(evict_team_kernel<ONE>, a.batch, team_smem(a.cap), kTeamSmem, cluster, st, a, 1, row);
     }
     // Teams of all SMs where a cluster's slices are long and SMs idle, or where large clusters do
     // not all fit at once (a GPC takes one or two of 8), unless k_out has no room for their counts.
@@ -546,12 +550,12 @@ cudaError_t select(const EvictArgs& a, int64_t keep, int row, cudaStream_t st) {
     const bool idle = team >= 2 * cs && a.cap > static_cast<int64_t>(cs) * 8192, crowd = cs >= 8 && a.batch * cs > 64;
     if (team > 1 && slice <= kKeys && (idle || crowd) &&
         keep * row >= 4 * (kScratchInts + 2 * static_cast<int64_t>(team)))
-        return launch_select(evict_team_kernel<GRID>, a.batch * team, team_smem(slice), coop, st, a, team, row);
+        return launch_select(evict_team_kernel<GRID>, a.batch * team, team_smem(slice), kTeamSmem, coop, st, a, team, row);
     cluster.val.clusterDim.x = cs;
     const int64_t part = (a.cap + cs - 1) / cs;
     if (part <= kKeys)
-        return launch_select(evict_team_kernel<CLUSTER>, a.batch * cs, team_smem(part), cluster, st, a, cs, row);
-    return launch_select(evict_select_kernel, a.batch * cs, kSelectSmem, cluster, st, a);
+        return launch_select(evict_team_kernel<CLUSTER>, a.batch * cs, team_smem(part), kTeamSmem, cluster, st, a, cs, row);
+    return launch_select(evict_select_kernel, a.batch * cs, kSelectSmem, kSelectSmem, cluster, st, a);
 }
 
 }  // namespace

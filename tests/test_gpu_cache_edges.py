@@ -3,6 +3,7 @@ in an input's place, two calls at once, captured calls, NaN and infinities in ro
 
 The forms, the checks and their tolerances are those of test_gpu_cache_ops.py."""
 import math
+import threading
 
 import pytest
 import torch
@@ -59,3 +60,61 @@ def test_evict_lengths_in_place(lens, cap, sinks, window, budget, kv):
     assert ins[0].tolist() == want[-1].tolist()
     for s, m in enumerate(want[-1].tolist()):
         assert outs[-2][s, :m].tolist() == list(range(m)) and (outs[-2][s, m:] == -1).all()
+
+
+# ------------------------------------------------------------------ two host threads
+def _threads(calls, times):
+    """Each call `times` times in a thread and on a stream of its own, all at once: the errors."""
+    errors, ready = [], threading.Barrier(len(calls))
+
+    def go(call, stream):
+        try:
+            torch.zeros(1, device="cuda")                      # the device's context is the thread's, too
+            ready.wait()
+            for _ in range(times):
+                call(stream)
+        except Exception as e:                                 # noqa: BLE001
+            errors.append(e)
+
+    torch.cuda.synchronize()
+    workers = [threading.Thread(target=go, args=(c, torch.cuda.Stream())) for c in calls]
+    for w in workers:
+        w.start()
+    for w in workers:
+        w.join()
+    torch.cuda.synchronize()
+    return errors
+
+
+@pytest.mark.parametrize("caps", [(1000, 16000), (20000, 140000)])
+def test_evictions_of_two_threads(caps):
+    """Selections whose shared memory differs, from two threads: each call is valid and is made."""
+    sets = [_evict_set(torch.rand(1, cap, generator=base._gen(cap)), [cap], 1, 9, 100, "e4m3", 64) for cap in caps]
+    for desc, ins, outs in sets:
+        hs.hs2_kv_evict(desc, *ins, *outs)
+    torch.cuda.synchronize()
+    want = [[None if t is None else t.clone() for t in outs] for _, _, outs in sets]
+    calls = [lambda st, s=s: hs.hs2_kv_evict(s[0], *s[1], *s[2], stream=st) for s in sets]
+    assert _threads(calls, 2000) == []
+    for (_, _, outs), ws in zip(sets, want):
+        assert all(t is None or torch.equal(t, w) for t, w in zip(outs, ws))
+
+
+def test_weight_calls_of_two_threads():
+    """16 and 64 pairs a sequence take query slots of different size in the same kernel."""
+    g = base._gen(12)
+    d, ctx, sets = 128, 600, []
+    k = torch.randn(1, ctx, d, generator=g).bfloat16().cuda()
+    for n in (1, 4):
+        q = torch.randn(1, n, 16, d, generator=g).bfloat16().cuda()
+        desc = hs.make_desc(1, n, 16, d, max_ctx=ctx)
+        sets.append((desc, q, k, None, torch.full((1, n, 16), 5.0, device="cuda"),
+                     torch.tensor([ctx - n], dtype=torch.int32, device="cuda"), None, 1.0, None,
+                     torch.zeros(1, ctx, device="cuda"), hs.alloc_accum_workspace(desc)))
+    for s in sets:
+        hs.hs2_weight_accum(*s)
+    torch.cuda.synchronize()
+    want = [s[-2].clone() for s in sets]
+    calls = [lambda st, s=s: hs.hs2_weight_accum(*s, stream=st) for s in sets]
+    assert _threads(calls, 3000) == []
+    assert all(torch.equal(s[-2], w) for s, w in zip(sets, want))
