@@ -382,8 +382,10 @@ cudaError_t launch_cand_select(const CandSelectArgs& in, cudaStream_t st) {
     a.map_words = words <= kMapWords ? static_cast<int>(words > 0 ? words : 1) : 0;
     const size_t sm = sizeof(Smem) + (a.map_words > 0 ? 4 * static_cast<size_t>(a.map_words)
                                                        : 4 * static_cast<size_t>(kFusedSelectMaxBudget));
+    // the function's limit, set to the largest that any call needs: calls of several threads set it
+    constexpr size_t most = sizeof(Smem) + 4 * static_cast<size_t>(kMapWords > kFusedSelectMaxBudget ? kMapWords : kFusedSelectMaxBudget);
     cudaError_t e = cudaFuncSetAttribute(cand_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(sm));
+                                         static_cast<int>(most));
     if (e != cudaSuccess) return e;
     cand_select_kernel<<<a.rows, CNT, sm, st>>>(a);
     return cudaGetLastError();

@@ -677,7 +677,10 @@ cudaError_t launch_impl(const SparseArgs& sa, cudaStream_t st) {
         return sa.rows <= kWideClusterRows ? launch(CShape<8>{}) : launch(CShape<4>{});
     }
     const size_t sm = smem_bytes<KV8>(pl.chunk);
-    e = cudaFuncSetAttribute(sparse_kernel<KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sm));
+    // the function's limit, set to the same value in every call (calls of several threads set it): a CTA's
+    // 227 KB less the 784 bytes of static arrays
+    constexpr int most = 232448 - 1024;
+    e = cudaFuncSetAttribute(sparse_kernel<KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     sparse_kernel<KV8><<<dim3(pl.splits, sa.rows), NT, sm, st>>>(a);
     return cudaGetLastError();

@@ -866,6 +866,14 @@ int pick_cluster(int rows, int64_t max_keys) {
 
 }  // namespace
 
+// Shared memory of a CTA with `cache_keys` keys in it (0: streamed), and the largest of any call.  The
+// limit that a launch needs belongs to the function in the whole process and calls of several threads set
+// it, so it is always set to the largest.
+constexpr size_t select_smem(int cache_keys) {
+    return (static_cast<size_t>(cache_keys) + 2 * kCandCap + (cache_keys == 0 ? 2 * NW * kWarpCap : 0)) * sizeof(uint32_t);
+}
+constexpr size_t kSelectSmem = select_smem(kSmemKeys) > select_smem(0) ? select_smem(kSmemKeys) : select_smem(0);
+
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t st) {
     if (a.rows <= 0) return cudaSuccess;
     const int bs = a.block_size < 1 ? 1 : a.block_size;
@@ -874,8 +882,7 @@ cudaError_t launch_select(const SelectArgs& a, cudaStream_t st) {
     for (;;) {
         const int64_t per = ((max_keys + cs - 1) / cs + 3) & ~int64_t(3);
         const int cache_keys = per <= kSmemKeys ? static_cast<int>(per) : 0;
-        const size_t smem = (static_cast<size_t>(cache_keys) + 2 * kCandCap + (cache_keys == 0 ? 2 * NW * kWarpCap : 0)) *
-                            sizeof(uint32_t);
+        const size_t smem = select_smem(cache_keys);
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * cs);
         cfg.blockDim = dim3(NT);
@@ -889,7 +896,7 @@ cudaError_t launch_select(const SelectArgs& a, cudaStream_t st) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         auto prepare = [&](auto kern) {
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSelectSmem));
             if (e == cudaSuccess && cs > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             return e;
         };
