@@ -118,3 +118,55 @@ def test_weight_calls_of_two_threads():
     calls = [lambda st, s=s: hs.hs2_weight_accum(*s, stream=st) for s in sets]
     assert _threads(calls, 3000) == []
     assert all(torch.equal(s[-2], w) for s, w in zip(sets, want))
+
+
+def _fresh_thread(call):
+    """A call made in a thread that has not used the device: its error, or None."""
+    errors = []
+
+    def go():
+        try:
+            call()
+        except Exception as e:                                 # noqa: BLE001
+            errors.append(e)
+
+    stream = torch.cuda.current_stream()
+    assert stream.cuda_stream is not None
+    torch.cuda.synchronize()
+    t = threading.Thread(target=go)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    return errors[0] if errors else None
+
+
+@pytest.mark.parametrize("n", [1, 20, 600])
+def test_calls_from_a_thread_that_has_not_used_the_device(n):
+    """Every call that describes its tiles to the copy engine, as a thread's first: the bits of the main
+    thread's call."""
+    g = base._gen(n)
+    b, h, d, ctx = 1, 16, 128, 2000
+    q, k, v = (torch.randn(*s, generator=g).bfloat16().cuda() for s in ((b, n, h, d), (b, ctx, d), (b, ctx, d)))
+    pos0 = torch.full((b,), ctx - n, dtype=torch.int32, device="cuda")
+    st = torch.cuda.current_stream()
+    desc = hs.make_desc(b, n, h, d, window=128, budget=256, max_ctx=ctx)
+    ws = [hs.alloc_window_workspace(desc, 2), hs.alloc_accum_workspace(desc), hs.alloc_workspace(desc)]
+    o, lse, acc = torch.empty_like(q), torch.empty(b, n, h, device="cuda"), torch.zeros(b, ctx, device="cuda")
+    idx, cnt = torch.empty(b, n, 384, dtype=torch.int32, device="cuda"), torch.empty(b, n, dtype=torch.int32, device="cuda")
+    x, w = torch.randn(b, n, 256, generator=g).bfloat16().cuda(), torch.randn(256, 256, generator=g).bfloat16().cuda()
+    kb, vb = torch.zeros_like(k), torch.zeros_like(v)
+    calls = {
+        "window": (lambda: hs.hs2_window_attn(desc, 2, q, k, v, None, None, pos0, None, o, lse, ws[0], stream=st), (o, lse)),
+        "accum": (lambda: hs.hs2_weight_accum(desc, q, k, None, lse, pos0, None, 1.0, None, acc, ws[1], stream=st), (acc,)),
+        "full": (lambda: hs.hs2_full_attn_select(desc, q, k, v, None, None, pos0, o, lse, idx, cnt, None, ws[2], stream=st),
+                 (o, lse, idx, cnt)),
+        "sparse": (lambda: hs.hs2_sparse_attn(desc, q, k, v, None, None, idx, cnt, o, lse, ws[2], stream=st), (o, lse)),
+        "bridge": (lambda: hs.hs2_kv_bridge_proj(x, w, b, n, 256, d, pos0, ctx, kb, vb, stream=st), (kb, vb)),
+    }
+    for name, (call, outs) in calls.items():
+        call()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in outs]
+        error = _fresh_thread(call)
+        assert error is None, (name, error)
+        assert all(torch.equal(t, x0) for t, x0 in zip(outs, want)), name
