@@ -39,18 +39,19 @@ struct Raw<float> {
     float4 a, b;
 };
 
-// The 8 dims of a lane: two groups of four, at d0 and d1.
+// The 8 dims of a lane: two groups of four, at d0 and d1.  Plain loads: q_out may be q, and the
+// read-only path is for memory that the kernel does not write.
 __device__ __forceinline__ void load8(Raw<__nv_bfloat16>& r, const __nv_bfloat16* x, int d0, int d1, bool together) {
     if (together) {
-        r.a = __ldg(reinterpret_cast<const uint4*>(x + d0));
+        r.a = *reinterpret_cast<const uint4*>(x + d0);
     } else {
-        const uint2 p = __ldg(reinterpret_cast<const uint2*>(x + d0)), q = __ldg(reinterpret_cast<const uint2*>(x + d1));
+        const uint2 p = *reinterpret_cast<const uint2*>(x + d0), q = *reinterpret_cast<const uint2*>(x + d1);
         r.a = make_uint4(p.x, p.y, q.x, q.y);
     }
 }
 __device__ __forceinline__ void load8(Raw<float>& r, const float* x, int d0, int d1, bool) {
-    r.a = __ldg(reinterpret_cast<const float4*>(x + d0));
-    r.b = __ldg(reinterpret_cast<const float4*>(x + d1));
+    r.a = *reinterpret_cast<const float4*>(x + d0);
+    r.b = *reinterpret_cast<const float4*>(x + d1);
 }
 __device__ __forceinline__ void widen(const Raw<__nv_bfloat16>& r, float (&v)[8]) {
     const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};

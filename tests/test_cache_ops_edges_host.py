@@ -75,3 +75,11 @@ def test_evict_refuses_outputs_over_one_another(L, kv):
                     assert _evict(L, kv, **{a: WHERE[b] + off}) == hs.HS2_ERR_INVALID_ARG, (a, b, off)
     assert _evict(L, kv, idx=WHERE["ko"] + BATCH * OUT * 128 * (1 if kv == hs.HS2_E4M3 else 2)) != hs.HS2_ERR_INVALID_ARG
     assert _evict(L, kv, new_len=WHERE["idx"] + BATCH * KEEP * 4) != hs.HS2_ERR_INVALID_ARG
+
+
+def test_rope_reads_its_rows_with_plain_loads():
+    """q_out may be q, so the rows' loads may not take the path for memory that the kernel does not write."""
+    src = os.path.join(os.path.dirname(os.path.abspath(hs.__file__)), "csrc", "rope_cache.cu")
+    loads = [body.split("\n}")[0] for body in open(src).read().split("void load8(")[1:]]
+    assert len(loads) == 2
+    assert all("__ldg" not in body and "reinterpret_cast<const" in body for body in loads)

@@ -170,3 +170,25 @@ def test_calls_from_a_thread_that_has_not_used_the_device(n):
         error = _fresh_thread(call)
         assert error is None, (name, error)
         assert all(torch.equal(t, x0) for t, x0 in zip(outs, want)), name
+
+
+# ------------------------------------------------------------------ rotation in place
+@pytest.mark.parametrize("b, n, h, d, rot, inter, dt", [
+    (2, 3, 16, 128, 128, False, "bf16"), (1, 700, 16, 128, 128, False, "bf16"), (2, 400, 5, 64, 48, False, "f32"),
+    (1, 650, 128, 64, 32, True, "bf16"), (3, 250, 7, 128, 96, False, "bf16"), (1, 5, 3, 64, 64, True, "f32"),
+    (1, 601, 9, 128, 128, False, "f32"),
+])
+def test_rope_in_place_gives_the_bits_of_a_call_apart(b, n, h, d, rot, inter, dt):
+    g = base._gen(n + h)
+    q = torch.randn(b, n, h, d, generator=g).to(base.DT[dt]).cuda()
+    w = (1 + 0.2 * torch.randn(d, generator=g)).cuda()
+    freq = (1e4 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)).cuda()
+    row0 = torch.arange(b, dtype=torch.int32, device="cuda")
+    desc = hs.make_rope_desc(b, n, h, d, rot_dim=rot, interleaved=inter, in_dtype=base.KIND[dt], kv_dtype=base.KIND[dt],
+                             kv_capacity=n)
+    out = torch.empty_like(q)
+    hs.hs2_qk_norm_rope(desc, q, None, None, w, None, freq, row0, None, None, out, None, None)
+    for _ in range(3):
+        x = q.clone()
+        hs.hs2_qk_norm_rope(desc, x, None, None, w, None, freq, row0, None, None, x, None, None)
+        assert torch.equal(x, out)
