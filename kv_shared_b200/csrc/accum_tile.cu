@@ -9,8 +9,7 @@
 // is a sum inside a thread.  A CTA holds a block of keys in shared memory and streams the
 // (row, head) pairs past it, so each key is read from HBM once and each Q tile from L2 once
 // per block.  Long calls are bound by the exponential unit (one exponential per key and pair,
-// 8 cycles a warp; a quarter of them moves to the FMA pipe, 6.7), calls of a few pairs by the
-// read of K.
+// 8 cycles a warp; an eighth of them moves to the FMA pipe), calls of a few pairs by the read of K.
 //
 // Two shapes of a work item (sequence, key block, part of the pairs):
 //   wide   2 x 128 keys, pairs in tiles of 128; two teams of warps take the tiles in turn, so
@@ -48,7 +47,10 @@ constexpr int NEXP = 16;                        // exponential warps
 constexpr int MK = 128;                         // keys per MMA
 constexpr int NL = 4;                           // tiles whose lse are held
 constexpr int kNarrow = 64;                     // most pairs of the narrow shape
-constexpr uint32_t kPolyGroups = 0x11;          // of 8 groups of 4 columns: which take the FMA pipe
+// Of 8 groups of 4 columns: which take the FMA pipe.  Two of them need more instructions than the
+// exponential unit saves: 32 rows of 16 heads over 4 x 131072 keys, bf16 and e4m3, 104 and 116 us, one 102
+// and 113.
+constexpr uint32_t kPolyGroups = 0x01;
 constexpr int kSmem = 232448;
 constexpr int kBars = 16 + 16 + 4 + 4 + 8 + 8 + NL + NL + 8;
 constexpr int OFF_XCH = 1024, OFF_NL = OFF_XCH + 4 * 2 * MK * 4, OFF_TILES = OFF_NL + NL * 2 * MK * 4;
@@ -138,14 +140,12 @@ __device__ __forceinline__ void add_weights(const uint32_t (&s)[W], const float*
         }
         const float2 x0 = fma2(make_float2(__uint_as_float(s[q]), __uint_as_float(s[q + 1])), ca, make_float2(n4.x, n4.y));
         const float2 x1 = fma2(make_float2(__uint_as_float(s[q + 2]), __uint_as_float(s[q + 3])), cb, make_float2(n4.z, n4.w));
-        float2 p0, p1;
         if (POLY && ((kPolyGroups >> (q / 4)) & 1u)) {
-            p0 = exp2_poly2(x0);
-            p1 = exp2_poly2(x1);
-        } else {
-            p0 = make_float2(ex2(x0.x), ex2(x0.y));
-            p1 = make_float2(ex2(x1.x), ex2(x1.y));
+            sum0 = add_exp2_poly2(x0, sum0);
+            sum1 = add_exp2_poly2(x1, sum1);
+            continue;
         }
+        float2 p0 = make_float2(ex2(x0.x), ex2(x0.y)), p1 = make_float2(ex2(x1.x), ex2(x1.y));
         if (!WHOLE) {
             p0.x = (see >> q) & 1u ? p0.x : 0.f;
             p0.y = (see >> (q + 1)) & 1u ? p0.y : 0.f;

@@ -1,5 +1,6 @@
 // f32x2.cuh -- fp32 arithmetic on pairs and 2^x on the FMA pipe, for the kernels around the
-// block that form many exponentials (prefill_attn.cu has its own, with the same coefficients).
+// block that form many exponentials (prefill_attn.cu has its own, with the same coefficients,
+// for arguments that are never above zero).
 #pragma once
 
 #include "common.cuh"
@@ -33,19 +34,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// 2^x for a pair on the FMA pipe (where the exponential unit is the bottleneck, a
+__device__ __forceinline__ float clamp_nan(float x, float lo, float hi) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(lo));
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(r) : "f"(hi));
+    return r;
+}
+
+// sum + 2^x for a pair on the FMA pipe (where the exponential unit is the bottleneck, a
 // share of the exponentials moves here): x = j + r with j the nearest integer (added to
 // and taken back from 1.5 * 2^23, whose ulp is 1) and r in [-1/2, 1/2]; 2^r by a degree-5
 // polynomial, the minimax relative-error fit of 2^r on that interval by Lawson's algorithm
 // (least squares reweighted by the error until it equioscillates; exp2_poly_fit.py beside
 // this package prints the coefficients): max relative error 2.1e-7 in fp32 Horner form,
-// like the exponential unit's; 2^j enters through the exponent bits.  x is clamped at -125 so
-// that the result stays a normal number (it is then below 2^-124, nothing beside the
-// row maximum's 1).
-__device__ __forceinline__ float2 exp2_poly2(float2 x) {
+// like the exponential unit's.  2^j, made of exponent bits, comes in with the addition, one
+// multiply-add: 0 below x = -126.5 and infinity from 127.5 up (between them j is -126 ..
+// 127), as fp32's own range ends, and a NaN stays one.  (Added to the polynomial's exponent
+// bits instead, j wrapped around for large x and a NaN came out as a number.)
+__device__ __forceinline__ float2 add_exp2_poly2(float2 x, float2 sum) {
     constexpr float kMagic = 12582912.f;                       // 1.5 * 2^23
-    x.x = fmaxf(x.x, -125.f);
-    x.y = fmaxf(x.y, -125.f);
+    x.x = clamp_nan(x.x, -127.f, 128.f);
+    x.y = clamp_nan(x.y, -127.f, 128.f);
     const float2 t = add2(x, make_float2(kMagic, kMagic));
     const float2 j = add2(t, make_float2(-kMagic, -kMagic));
     const float2 r = add2(x, make_float2(-j.x, -j.y));
@@ -55,8 +64,10 @@ __device__ __forceinline__ float2 exp2_poly2(float2 x) {
     p = fma2(p, r, make_float2(2.4022120e-1f, 2.4022120e-1f));
     p = fma2(p, r, make_float2(6.9314694e-1f, 6.9314694e-1f));
     p = fma2(p, r, make_float2(1.0000001f, 1.0000001f));
-    return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
-                       __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+    // exponent bits j + 127 in [0, 255] (kMagic's lower bits are zero)
+    const float2 s = make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3f800000),
+                                 __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000));
+    return fma2(p, s, sum);
 }
 
 }  // namespace hs2

@@ -192,3 +192,76 @@ def test_rope_in_place_gives_the_bits_of_a_call_apart(b, n, h, d, rot, inter, dt
         x = q.clone()
         hs.hs2_qk_norm_rope(desc, x, None, None, w, None, freq, row0, None, None, x, None, None)
         assert torch.equal(x, out)
+
+
+# ------------------------------------------------------------------ weights: NaN and infinities in use
+ACCUM_FORMS = [  # rows, heads, kv: wide and narrow tiles of pairs, fp32
+    (16, 16, "bf16"), (16, 16, "e4m3"), (4, 16, "bf16"), (4, 16, "e4m3"), (9, 8, "f32"), (2, 5, "f32"), (60, 5, "bf16"),
+]
+
+
+def _accum_case(n, h, kv, ctx=700, d=128):
+    """(q, k, ks, lse, pos0, kk, logits): a prompt's last n rows, logits [n, h, ctx] in fp64, hidden ones -inf."""
+    g = base._gen(n * h)
+    q = torch.randn(1, n, h, d, generator=g).to(base.DT["f32" if kv == "f32" else "bf16"])
+    k, _, ks, _ = base._cache(g, 1, ctx, d, kv)
+    kk = ref.wide(k[0], None if ks is None else ks[0])
+    x = torch.einsum("rhd,kd->rhk", q[0].double(), kk) * d ** -0.5
+    hide = torch.arange(ctx) > ctx - n + torch.arange(n)[:, None]
+    x = x.masked_fill(hide[:, None], -math.inf)
+    return q, k, ks, x.logsumexp(-1).float()[None], torch.tensor([ctx - n], dtype=torch.int32), x
+
+
+def _accum_of(q, k, ks, lse, pos0, kv):
+    n, h, d = q.shape[1:]
+    desc = hs.make_desc(1, n, h, d, q_dtype=base.KIND["f32" if kv == "f32" else "bf16"], kv_dtype=base.KIND[kv],
+                        max_ctx=k.shape[1])
+    ws, out = hs.alloc_accum_workspace(desc), torch.full((1, k.shape[1]), -3.0, device="cuda")
+    hs.hs2_weight_accum(desc, *base._cu(q, k, ks, lse, pos0, None), 1.0, None, out, ws)
+    assert hs.hs2_last_status(ws) == hs.HS2_OK
+    return out[0].cpu()
+
+
+@pytest.mark.parametrize("n, h, kv", ACCUM_FORMS)
+@pytest.mark.parametrize("where", ["query", "lse"])
+def test_accum_keeps_a_nan(n, h, kv, where):
+    """A NaN in a pair's query or lse is in the total of every key that the pair sees, whichever pair it is."""
+    q, k, ks, lse, pos0, _ = _accum_case(n, h, kv)
+    base_out = _accum_of(q, k, ks, lse, pos0, kv)
+    assert base_out.isfinite().all()
+    for f in sorted({*range(min(n * h, 40)), n * h // 2, n * h - 1}):
+        q2, l2 = q.clone(), lse.clone()
+        if where == "query":
+            q2[0, f // h, f % h, 3] = math.nan
+        else:
+            l2[0, f // h, f % h] = math.nan
+        got, p = _accum_of(q2, k, ks, l2, pos0, kv), int(pos0[0]) + f // h
+        assert got[:p + 1].isnan().all() and torch.equal(got[p + 1:], base_out[p + 1:]), f
+
+
+@pytest.mark.parametrize("n, h, kv", ACCUM_FORMS)
+def test_accum_of_an_lse_that_leaves_keys_out(n, h, kv):
+    """An lse far below a pair's logits (of a layer whose rows leave keys out, say): weights up to 2^100
+    are numbers, those past fp32's range infinite; an infinite lse makes them zero."""
+    q, k, ks, lse, pos0, x = _accum_case(n, h, kv)
+    ends = torch.arange(x.shape[2])
+    for f in sorted({*range(min(n * h, 36)), n * h - 1}):
+        r, p = f // h, int(pos0[0]) + f // h
+        for shift, want in ((100.0, None), (140.0, math.inf), (400.0, math.inf)):
+            l2 = lse.clone()
+            l2[0, r, f % h] = x[r, f % h, :p + 1].min() - shift * math.log(2.0)
+            if shift == 100.0:                              # weights of one pair from 2^100 up
+                l2[0, r, f % h] = x[r, f % h, :p + 1].max() - shift * math.log(2.0)
+            got = _accum_of(q, k, ks, l2, pos0, kv)[:p + 1].double()
+            if want is not None:
+                assert (got == want).all(), (f, shift)
+                continue
+            ref_w = (x[r, f % h, :p + 1] - l2[0, r, f % h].double()).exp()
+            # the other pairs' weights, each at most one, are below 2^-60 of it; the exponent's own
+            # rounding 2^-24 of |logit| + |lse| (below 2^8) in log2 units, the products' 2 d 2^-24 of 2^6
+            rel = (2 * 128 * 64 + 8 * 256) * 2.0 ** -24
+            assert ((got - ref_w).abs() <= rel * ref_w + n * h).all(), f
+        l2 = torch.full_like(lse, math.inf)
+        assert (_accum_of(q, k, ks, l2, pos0, kv)[ends < int(pos0[0]) + n] == 0).all()
+
+
