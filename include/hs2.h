@@ -356,8 +356,9 @@ HS2_API size_t hs2_weight_accum_workspace_size(const hs2_attn_desc* desc);
  * rows of a prompt alone, or one new token, are ordinary uses).  acc_in, acc_out:
  * [batch][kv_capacity] fp32; acc_in may be acc_out, or NULL for zeros (decay is then
  * unused); decay >= 0.  E4M3 caches: query elements below 2^-9 of their row's largest are
- * rounded to 2^-17 of it.  desc->window, budget and idx_stride are not used.  The sums'
- * order is fixed by the sizes: equal calls give equal bits.
+ * rounded to 2^-17 of it, and a row with an infinite element counts as NaN.
+ * desc->window, budget and idx_stride are not used.  The sums' order is fixed by the
+ * sizes: equal calls give equal bits.
  */
 HS2_API hs2_status hs2_weight_accum(const hs2_attn_desc* desc, const void* q, const void* k,
                                     const float* k_scale, const float* lse, const int32_t* q_pos0,

@@ -466,7 +466,8 @@ __global__ void __launch_bounds__(256) accum_split_q_kernel(const __nv_bfloat16*
         *reinterpret_cast<uint32_t*>(dst) = hi[0];
         *reinterpret_cast<uint32_t*>(dst + D) = lo[0];
     }
-    if (l == 0) scale[row] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    // a row with an infinity, which e4m3 has no code for: NaN for the whole row, not its largest codes
+    if (l == 0) scale[row] = ex == 128 ? __int_as_float(0x7fffffff) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
 
 template <int D, bool KV8, bool NARROW>

@@ -265,3 +265,14 @@ def test_accum_of_an_lse_that_leaves_keys_out(n, h, kv):
         assert (_accum_of(q, k, ks, l2, pos0, kv)[ends < int(pos0[0]) + n] == 0).all()
 
 
+@pytest.mark.parametrize("n", [4, 16])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf])
+def test_accum_of_an_infinite_query(n, bad):
+    """Next to e4m3 keys a query goes in as finite codes: a row with an infinity gives NaN, not numbers."""
+    q, k, ks, lse, pos0, _ = _accum_case(n, 16, "e4m3")
+    clean = _accum_of(q, k, ks, lse, pos0, "e4m3")
+    for f in (0, 5, 33, n * 16 - 1):
+        q2 = q.clone()
+        q2[0, f // 16, f % 16, 100] = bad
+        got, p = _accum_of(q2, k, ks, lse, pos0, "e4m3"), int(pos0[0]) + f // 16
+        assert got[:p + 1].isnan().all() and torch.equal(got[p + 1:], clean[p + 1:]), f
