@@ -134,6 +134,8 @@ __global__ void __launch_bounds__(NT) rope_cache_kernel(RopeArgs a, int wpr, int
         }
         __syncwarp();
     }
+    // dims past rot (a multiple of 16: all eight of a lane) keep their partners out, 0 * infinity being NaN
+    const bool still = MODE != HALVES && d0 >= rot;
     // PARTIAL: the partner's lane, half a rotation (a multiple of 8 dims) up or down
     const int from = MODE == PARTIAL && d0 < rot ? lane + (d0 < half ? half >> 3 : -(half >> 3)) : lane;
     // out[i] = inv (x[i] c[i] + x[partner of i] s[i]): cosine and signed sine times the weights
@@ -179,8 +181,9 @@ __global__ void __launch_bounds__(NT) rope_cache_kernel(RopeArgs a, int wpr, int
         const float2 z = make_float2(0.f, 0.f), i2 = make_float2(inv, inv);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            const float2 near = fma2(make_float2(y[i], y[i + 1]), c[i / 2], z);
-            const float2 t = fma2(fma2(make_float2(o[i], o[i + 1]), s[i / 2], near), i2, z);
+            float2 t = fma2(make_float2(y[i], y[i + 1]), c[i / 2], z);
+            if (!still) t = fma2(make_float2(o[i], o[i + 1]), s[i / 2], t);
+            t = fma2(t, i2, z);
             x[i] = t.x;
             x[i + 1] = t.y;
         }

@@ -276,3 +276,35 @@ def test_accum_of_an_infinite_query(n, bad):
         q2[0, f // 16, f % 16, 100] = bad
         got, p = _accum_of(q2, k, ks, lse, pos0, "e4m3"), int(pos0[0]) + f // 16
         assert got[:p + 1].isnan().all() and torch.equal(got[p + 1:], clean[p + 1:]), f
+
+
+# ------------------------------------------------------------------ rotation: infinities
+@pytest.mark.parametrize("rot, inter", [(0, False), (0, True), (32, False), (32, True), (96, False), (96, True), (128, False)])
+@pytest.mark.parametrize("dt, kv", [("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("normalize", [False, True])
+def test_rope_keeps_an_infinity_in_its_place(rot, inter, dt, kv, normalize):
+    """An infinity or NaN in a dim that does not turn stays in that dim (without a norm); in a pair that
+    turns it reaches the pair's other dim and no further."""
+    g = base._gen(rot)
+    n, h, d = 6, 3, 128
+    q0, k0 = (torch.randn(1, n, x, d, generator=g).to(base.DT[dt]) for x in (h, 1))
+    bad = [(0, 127, math.inf), (1, 100, -math.inf), (2, 5, math.inf), (3, 64, math.nan), (4, 31, math.inf)]
+    for r, i, x in bad:
+        q0[0, r, r % h, i] = x
+        k0[0, r, 0, i] = x
+    freq = 1e4 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1))
+    row0 = torch.tensor([11], dtype=torch.int32)
+    q, k, fr, r0 = base._cu(q0, k0, freq, row0)
+    out, kc = torch.empty_like(q), torch.zeros(1, 32, d, dtype=base.DT[kv], device="cuda")
+    desc = hs.make_rope_desc(1, n, h, d, rot_dim=rot, interleaved=inter, normalize=normalize, in_dtype=base.KIND[dt],
+                             kv_dtype=base.KIND[kv], kv_capacity=32)
+    hs.hs2_qk_norm_rope(desc, q, k, None, None, None, fr if rot else None, r0, None, None, out, kc, None)
+    torch.cuda.synchronize()
+    for got, src in ((out[0].cpu().double(), q0[0]), (kc[0, 11:11 + n, None].cpu().double(), k0[0])):
+        want = ref.norm_rope(src, None, 1e-6, [11 + t for t in range(n)], freq, inter, normalize=normalize)
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+        assert torch.equal(got[got.isinf()], want[want.isinf()])
+        ok = want.isfinite()
+        top = torch.where(ok, want.abs(), torch.zeros_like(want)).amax(-1, keepdim=True)
+        half = base.HALF_BF16 if dt == "bf16" else 0.0
+        assert ((got - want).abs() <= half * want.abs() + 2.0 ** -18 * top)[ok].all()
