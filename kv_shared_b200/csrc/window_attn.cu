@@ -324,7 +324,8 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a, F
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
         if (t == 0) {
-            s_m[warp * 16 + g + 8 * r] = m[r];
+            // a NaN query leaves no maximum, but a sum that is to be joined: any number serves as its reference
+            s_m[warp * 16 + g + 8 * r] = l[r] != l[r] ? 0.f : m[r];
             s_l[warp * 16 + g + 8 * r] = l[r];
         }
     }
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(D / 4 * JOIN_Y) window_join_kernel(WindowArgs 
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            if (ml[i].x == -INFINITY) continue;                  // a part without keys may have left no O
+            if (ml[i].y == 0.f) continue;                        // a part without keys may have left no O (NaN: a NaN query's)
             const float mn = fmaxf(mx, ml[i].x), c0 = exp2f(mx - mn), c1 = exp2f(ml[i].x - mn);
             sum = fmaf(sum, c0, c1 * ml[i].y);
             acc.x = fmaf(acc.x, c0, c1 * x[i].x); acc.y = fmaf(acc.y, c0, c1 * x[i].y);
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(D / 4 * JOIN_Y) window_join_kernel(WindowArgs 
     acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < JOIN_Y; ++i) {
-        const float c = s_ml[i].x == -INFINITY ? 0.f : exp2f(s_ml[i].x - mx);
+        const float c = s_ml[i].y == 0.f ? 0.f : exp2f(s_ml[i].x - mx);
         const float4 x = s_o[i][threadIdx.x];
         sum = fmaf(c, s_ml[i].y, sum);
         acc.x = fmaf(c, x.x, acc.x); acc.y = fmaf(c, x.y, acc.y);

@@ -308,3 +308,36 @@ def test_rope_keeps_an_infinity_in_its_place(rot, inter, dt, kv, normalize):
         top = torch.where(ok, want.abs(), torch.zeros_like(want)).amax(-1, keepdim=True)
         half = base.HALF_BF16 if dt == "bf16" else 0.0
         assert ((got - want).abs() <= half * want.abs() + 2.0 ** -18 * top)[ok].all()
+
+
+# ------------------------------------------------------------------ sliding window: NaN queries
+@pytest.mark.parametrize("n, window, kv", [
+    (1, 100, "bf16"), (1, 100, "e4m3"), (1, 2000, "bf16"), (1, 2000, "e4m3"), (20, 100, "bf16"), (20, 1800, "e4m3"),
+    (600, 100, "bf16"), (300, 1800, "bf16"), (600, 100, "e4m3"), (300, 1800, "e4m3"), (1, 100, "f32"), (1, 2000, "f32"),
+    (40, 300, "f32"), (700, 100, "f32"),
+])
+def test_window_keeps_a_nan_query(n, window, kv):
+    """A NaN in a row's query is in that row's output and lse and in no other's."""
+    g = base._gen(n + window)
+    b, h, d, ctx = 2, 16, 128, 2500
+    dt = base.DT["f32" if kv == "f32" else "bf16"]
+    q = torch.randn(b, n, h, d, generator=g).to(dt)
+    k, v, ks, vs = base._cache(g, b, ctx, d, kv)
+    pos0 = torch.tensor([ctx - n, min(1900, ctx - n)], dtype=torch.int32)
+    bad = n // 2
+    q[0, bad, :, 7] = math.nan
+    dev = base._cu(q, k, v, ks, vs, pos0, None)
+    o, lse = torch.zeros_like(dev[0]), torch.zeros(b, n, h, device="cuda")
+    desc = hs.make_desc(b, n, h, d, window=window, budget=0, q_dtype=base.KIND["f32" if kv == "f32" else "bf16"],
+                        kv_dtype=base.KIND[kv], max_ctx=ctx)
+    ws = hs.alloc_window_workspace(desc, 3)
+    hs.hs2_window_attn(desc, 3, *dev, o, lse, ws)
+    assert hs.hs2_last_status(ws) == hs.HS2_OK
+    assert o[0, bad].isnan().all() and lse[0, bad].isnan().all()
+    assert int(o.isnan().sum()) == h * d and int(lse.isnan().sum()) == h
+    near = [r for r in (0, bad - 1, bad + 1, n - 1) if 0 <= r < n]
+    for s in range(b):
+        rows = [r for r in near if s or r != bad]
+        base._check_window(q[s:s + 1], k[s:s + 1], v[s:s + 1], None if ks is None else ks[s:s + 1],
+                           None if vs is None else vs[s:s + 1], pos0[s:s + 1], None, window, 3, o[s:s + 1].cpu(),
+                           lse[s:s + 1].cpu(), kv, 0, rows=rows)
