@@ -27,7 +27,8 @@
  *     and never synchronizes, except hs2_last_status.
  *   - Every compute call only validates its arguments on the host and enqueues
  *     kernels on `stream` (NULL = the legacy default stream); it returns before
- *     the work runs.
+ *     the work runs.  The work runs on the current device, whose `stream` and
+ *     memory it is given.
  *   - Layouts are row-major and contiguous:
  *       Q, O          [batch][n_q][heads][head_dim]
  *       K, V cache    [batch][kv_capacity][head_dim]   (one K/V head shared by all

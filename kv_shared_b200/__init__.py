@@ -4,7 +4,7 @@ Argument marshalling only: every function below forwards torch tensors (device
 memory) and the current CUDA stream to the C ABI declared in include/hs2.h, with
 the same names, and raises HS2Error on a non-OK status (through ctypes; the calls
 around the block, some of which run for a few microseconds, through csrc/calls.c).  All computation runs in
-the CUDA kernels of libhs2.so; there is no fallback.  Build the library with
+the CUDA kernels of libhs2.so, on the current device; there is no fallback.  Build the library with
 ``python -m kv_shared_b200.build`` (or ``__graft_entry__.build()``).
 """
 import ctypes
@@ -46,9 +46,9 @@ class hs2_evict_desc(ctypes.Structure):
 
 
 class HS2Error(RuntimeError):
-    def __init__(self, fn, status):
+    def __init__(self, fn, status, why=""):
         self.status = status
-        super().__init__(f"{fn}: {status_string(status)} ({status})")
+        super().__init__(f"{fn}: {status_string(status)} ({status})" + (f": {why}" if why else ""))
 
 
 _lib = None
@@ -129,6 +129,23 @@ _current_stream = _current_stream_getter(torch._C)
 
 def _stream(stream=None):
     return _current_stream() if stream is None else stream.cuda_stream
+
+
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _stream_here(fn, stream, t):
+    """_stream for a call around the block.  Its kernels run on the current device, where another device's
+    or the host's memory is a fault, so one tensor of the call, t, is looked at (all of them would cost a
+    single token's call a tenth of its time).  Beside a given stream only another device is refused."""
+    if stream is None:
+        if t is not None and t.get_device() != _device():
+            raise HS2Error(fn, HS2_ERR_INVALID_ARG, "a tensor is not on the current device")
+        return _current_stream()
+    d = getattr(t, "get_device", lambda: -1)()
+    if d >= 0 and (d != _device() or d != getattr(stream, "device_index", d)):
+        raise HS2Error(fn, HS2_ERR_INVALID_ARG, "a tensor or the stream is not on the current device")
+    return stream.cuda_stream
 
 
 def _check(fn, status):
@@ -237,7 +254,7 @@ def make_evict_desc(batch, head_dim, kv_dtype=HS2_BF16, sinks=0, window=128, bud
 def hs2_qk_norm_rope(desc, q, k, v, q_weight, k_weight, inv_freq, row0, pos, n_rows, q_out, k_cache, v_cache,
                      k_scale=None, v_scale=None, stream=None):
     st = _fast().qk_norm_rope(desc, q, k, v, q_weight, k_weight, inv_freq, row0, pos, n_rows, q_out, k_cache, v_cache,
-                              k_scale, v_scale, _stream(stream))
+                              k_scale, v_scale, _stream_here("hs2_qk_norm_rope", stream, row0))
     _check("hs2_qk_norm_rope", st)
 
 
@@ -247,7 +264,7 @@ def hs2_window_workspace_size(desc, sinks=0):
 
 def hs2_window_attn(desc, sinks, q, k, v, k_scale, v_scale, q_pos0, n_rows, o, lse, workspace, stream=None):
     st = _fast().window_attn(desc, int(sinks), q, k, v, k_scale, v_scale, q_pos0, n_rows, o, lse, workspace,
-                             workspace.numel() * workspace.element_size(), _stream(stream))
+                             workspace.numel() * workspace.element_size(), _stream_here("hs2_window_attn", stream, q_pos0))
     _check("hs2_window_attn", st)
 
 
@@ -257,14 +274,14 @@ def hs2_weight_accum_workspace_size(desc):
 
 def hs2_weight_accum(desc, q, k, k_scale, lse, q_pos0, n_rows, decay, acc_in, acc_out, workspace, stream=None):
     st = _fast().weight_accum(desc, q, k, k_scale, lse, q_pos0, n_rows, decay, acc_in, acc_out, workspace,
-                              workspace.numel() * workspace.element_size(), _stream(stream))
+                              workspace.numel() * workspace.element_size(), _stream_here("hs2_weight_accum", stream, q_pos0))
     _check("hs2_weight_accum", st)
 
 
 def hs2_kv_evict(desc, len_, acc, k, v, k_scale, v_scale, k_out, v_out, k_scale_out, v_scale_out, acc_out, idx,
                  new_len, stream=None):
     st = _fast().kv_evict(desc, len_, acc, k, v, k_scale, v_scale, k_out, v_out, k_scale_out, v_scale_out, acc_out, idx,
-                          new_len, _stream(stream))
+                          new_len, _stream_here("hs2_kv_evict", stream, len_))
     _check("hs2_kv_evict", st)
 
 
