@@ -341,3 +341,126 @@ def test_window_keeps_a_nan_query(n, window, kv):
         base._check_window(q[s:s + 1], k[s:s + 1], v[s:s + 1], None if ks is None else ks[s:s + 1],
                            None if vs is None else vs[s:s + 1], pos0[s:s + 1], None, window, 3, o[s:s + 1].cpu(),
                            lse[s:s + 1].cpu(), kv, 0, rows=rows)
+
+
+# ------------------------------------------------------------------ bounds of padded batches
+@pytest.mark.parametrize("n, kv", [(1, "bf16"), (3, "e4m3"), (40, "bf16"), (700, "bf16"), (700, "e4m3"), (5, "f32"), (90, "f32")])
+def test_row_counts_outside_the_batch_are_clamped(n, kv):
+    """n_rows below 0 and above n: the bits of calls with 0 and n."""
+    g = base._gen(n)
+    b, h, d, ctx = 3, 16, 128, 1500
+    dt = base.DT["f32" if kv == "f32" else "bf16"]
+    qd = base.KIND["f32" if kv == "f32" else "bf16"]
+    q, k0, v0 = (torch.randn(b, n, x, d, generator=g).to(dt).cuda() for x in (h, 1, 1))
+    k, v, ks, vs = base._cu(*base._cache(g, b, ctx, d, kv))
+    pos0 = torch.tensor([ctx - n, 100, 3], dtype=torch.int32, device="cuda")
+    freq = (1e4 ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)).cuda()
+    lse0 = torch.full((b, n, h), 4.0, device="cuda")
+    rd = hs.make_rope_desc(b, n, h, d, in_dtype=qd, kv_dtype=base.KIND[kv], kv_capacity=ctx)
+    desc = hs.make_desc(b, n, h, d, window=200, budget=0, q_dtype=qd, kv_dtype=base.KIND[kv], max_ctx=ctx)
+    ws, aws = hs.alloc_window_workspace(desc, 3), hs.alloc_accum_workspace(desc)
+
+    def run(counts):
+        rows = torch.tensor(counts, dtype=torch.int32, device="cuda")
+        out = dict(q=torch.full_like(q, 7.0), kc=torch.zeros_like(k), vc=torch.zeros_like(v),
+                   ks=None if ks is None else torch.zeros_like(ks), vs=None if vs is None else torch.zeros_like(vs),
+                   o=torch.full_like(q, 7.0), lse=torch.full_like(lse0, 7.0), acc=torch.full((b, ctx), 7.0, device="cuda"))
+        hs.hs2_qk_norm_rope(rd, q, k0, v0, None, None, freq, pos0, None, rows, out["q"], out["kc"], out["vc"], out["ks"],
+                            out["vs"])
+        hs.hs2_window_attn(desc, 3, q, k, v, ks, vs, pos0, rows, out["o"], out["lse"], ws)
+        hs.hs2_weight_accum(desc, q, k, ks, lse0, pos0, rows, 1.0, None, out["acc"], aws)
+        assert hs.hs2_last_status(ws) == hs.HS2_OK and hs.hs2_last_status(aws) == hs.HS2_OK
+        return out
+
+    for counts, clamped in (([-3, n + 5, n], [0, n, n]), ([-(1 << 31), (1 << 31) - 1, -1], [0, n, 0])):
+        want, got = run(clamped), run(counts)
+        for key, t in want.items():
+            assert t is None or torch.equal(t, got[key]), (key, counts)
+
+
+@pytest.mark.parametrize("n, window, ctx, ragged", [(1, 100, 900, False), (1, 3000, 5000, False), (20, 60, 900, True),
+                                                    (600, 100, 1300, False), (300, 33, 800, True)])
+def test_scales_of_rows_out_of_use_may_be_nan(n, window, ctx, ragged):
+    """e4m3 rows that no query attends to: codes and scales hold NaN; results as with numbers there."""
+    g = base._gen(n + ctx)
+    b, h, d, sinks = 4, 16, 128, 5
+    q = torch.randn(b, n, h, d, generator=g).to(torch.bfloat16)
+    k, v, ks, vs = base._cache(g, b, ctx, d, "e4m3")
+    pos0 = torch.tensor([ctx - n, 0, 300 % (ctx - n + 1), 57 % (ctx - n + 1)], dtype=torch.int32)
+    counts = [n, 0, n // 2, 1] if ragged else [n] * b
+    rows = torch.tensor(counts, dtype=torch.int32) if ragged else None
+    seen, past = torch.zeros(b, ctx, dtype=torch.bool), torch.zeros(b, ctx, dtype=torch.bool)
+    for s, m in enumerate(counts):
+        past[s, int(pos0[s]) + m:] = True
+        if m:
+            seen[s, max(0, int(pos0[s]) - window + 1):int(pos0[s]) + m] = True
+            seen[s, :min(sinks, int(pos0[s]) + m)] = True
+    desc = hs.make_desc(b, n, h, d, window=window, budget=0, kv_dtype=hs.HS2_E4M3, max_ctx=ctx)
+    ws, aws = hs.alloc_window_workspace(desc, sinks), hs.alloc_accum_workspace(desc)
+    lse_in = torch.full((b, n, h), 5.0)
+    got = []
+    for mask_w, mask_a in ((~seen, past), (torch.zeros_like(seen), torch.zeros_like(past))):
+        kw, vw, ka = (base._poison(t, m) for t, m in ((k, mask_w), (v, mask_w), (k, mask_a)))
+        sw, tw, sa = (torch.where(m, torch.full_like(t, math.nan), t) for t, m in ((ks, mask_w), (vs, mask_w), (ks, mask_a)))
+        o, lse = torch.full((b, n, h, d), 7.0, device="cuda").bfloat16(), torch.full((b, n, h), 7.0, device="cuda")
+        acc = torch.full((b, ctx), 7.0, device="cuda")
+        hs.hs2_window_attn(desc, sinks, *base._cu(q, kw, vw, sw, tw, pos0, rows), o, lse, ws)
+        hs.hs2_weight_accum(desc, *base._cu(q, ka, sa, lse_in, pos0, rows), 1.0, None, acc, aws)
+        assert hs.hs2_last_status(ws) == hs.HS2_OK and hs.hs2_last_status(aws) == hs.HS2_OK
+        got.append((o, lse, acc))
+    for x, y in zip(*got):
+        assert x.isfinite().all() and torch.equal(x, y)
+
+
+# ------------------------------------------------------------------ eviction by teams of all SMs
+def test_evict_by_teams_in_a_graph_and_beside_another_stream():
+    """The grid-wide selection captured and replayed on other lengths and totals, and run while another
+    stream works: the bits of the call made alone."""
+    g = base._gen(77)
+    cap, lens = 300000, [300000, 150001]
+    desc, ins, outs = _evict_set(torch.rand(2, cap, generator=g), lens, 3, 64, 60000, "e4m3", 64)
+
+    def alone():
+        hs.hs2_kv_evict(desc, *ins, *outs)
+        torch.cuda.synchronize()
+        return [t.clone() for t in outs]
+
+    first = alone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hs.hs2_kv_evict(desc, *ins, *outs)
+    ins[1].copy_(torch.rand(2, cap, generator=g))
+    ins[0].copy_(torch.tensor([299001, 60000], dtype=torch.int32))
+    want = alone()
+    assert not torch.equal(first[-2], want[-2])
+    for _ in range(3):
+        for t in outs:
+            t.fill_(9)
+        graph.replay()
+        torch.cuda.synchronize()
+        for s, m in enumerate(want[-1].tolist()):
+            assert all(torch.equal(t[s, :m], w[s, :m]) for t, w in zip(outs[:-1], want[:-1]))
+        assert torch.equal(outs[-1], want[-1]) and torch.equal(outs[-2], want[-2])
+    # beside weight calls and evictions of another form on a second stream
+    q, kb = torch.randn(2, 8, 16, 128, generator=g).bfloat16().cuda(), torch.randn(2, 20000, 128, generator=g).bfloat16().cuda()
+    ad = hs.make_desc(2, 8, 16, 128, max_ctx=20000)
+    a_in = (q, kb, None, torch.full((2, 8, 16), 9.0, device="cuda"), torch.full((2,), 19992, dtype=torch.int32, device="cuda"), None)
+    acc, aws = torch.zeros(2, 20000, device="cuda"), hs.alloc_accum_workspace(ad)
+    small = _evict_set(torch.rand(3, 9000, generator=g), [9000, 8000, 7], 1, 5, 700, "bf16", 64)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for t in outs:
+        t.fill_(9)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        hs.hs2_kv_evict(desc, *ins, *outs, stream=streams[0])
+        hs.hs2_weight_accum(ad, *a_in, 1.0, None, acc, aws, stream=streams[1])
+        hs.hs2_kv_evict(small[0], *small[1], *small[2], stream=streams[1])
+    torch.cuda.synchronize()
+    for s, m in enumerate(want[-1].tolist()):
+        assert all(torch.equal(t[s, :m], w[s, :m]) for t, w in zip(outs[:-1], want[:-1]))
+    beside = [acc.clone(), *[None if t is None else t.clone() for t in small[2]]]
+    hs.hs2_weight_accum(ad, *a_in, 1.0, None, acc, aws)
+    hs.hs2_kv_evict(small[0], *small[1], *small[2])
+    for x, y in zip(beside, [acc, *small[2]]):
+        assert x is None or torch.equal(x, y)
