@@ -336,7 +336,8 @@ HS2_API size_t hs2_window_workspace_size(const hs2_attn_desc* desc, int32_t sink
  * counts once), sinks >= 0.  o = softmax(softmax_scale q k^T) v over those rows,
  * lse (optional) the log of the sum.  Serves single tokens (n_q = 1) and chunks.
  * desc->budget and idx_stride are not used.  Cache rows that no query of the call
- * attends to may hold anything; the rows that some query attends to must be finite.
+ * attends to may hold anything; the rows that some query attends to must be finite,
+ * and their value scales (E4M3) between 2^-60 and 2^60.
  * A query position outside [0, max_ctx) is clamped into it and reported as
  * HS2_ERR_INDEX.
  */
@@ -389,6 +390,8 @@ typedef struct {
  * ascending, then -1.  Output rows from new_len[b] on are left as they were.
  *   len      device int32 [batch], clamped to [0, kv_capacity]
  *   acc      [batch][kv_capacity] fp32; acc_out optional [batch][out_capacity]
+ * The selection's launches and buffers go by kv_capacity, whatever the lengths are: a few
+ * rows in a cache of a million cost the barriers of a selection over a million.
  * new_len may be len itself; any other output that overlaps an input or another output
  * is refused (HS2_ERR_INVALID_ARG).  No workspace.
  */

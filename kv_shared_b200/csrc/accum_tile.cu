@@ -26,8 +26,9 @@
 // ones exactly, down to elements 2^-9 of the row's largest; smaller ones are rounded to 2^-17
 // of it at worst.
 //
-// Measured: 32 rows of 16 heads over 4 x 131072 bf16 keys 93 us (740 TFLOP/s; exponentials and
-// their arithmetic alone would take 50), one row over 8 x 100001 e4m3 keys 25.9 us (4.3 TB/s).
+// Measured, replayed from a graph on the same inputs: 32 rows of 16 heads over 4 x 131072 bf16
+// keys 92 us (750 TFLOP/s; exponentials and their arithmetic alone would take 50), one row over
+// 8 x 100001 e4m3 keys 25.5 us (4.3 TB/s).  As calls among others on changing inputs: 104.6 and 28.5.
 //
 // Roles (640 threads): warps 0-15 exponentials, 16 the TMA loads, 17 the pairs' lse (and
 // scales), 18 and 19 the MMAs of the even and the odd 128 keys.  Every wait is bounded; a
@@ -48,8 +49,8 @@ constexpr int MK = 128;                         // keys per MMA
 constexpr int NL = 4;                           // tiles whose lse are held
 constexpr int kNarrow = 64;                     // most pairs of the narrow shape
 // Of 8 groups of 4 columns: which take the FMA pipe.  Two of them need more instructions than the
-// exponential unit saves: 32 rows of 16 heads over 4 x 131072 keys, bf16 and e4m3, 104 and 116 us, one 102
-// and 113.
+// exponential unit saves: 32 rows of 16 heads over 4 x 131072 keys, bf16 and e4m3, 104 and 116 us a call,
+// one 102 and 113.
 constexpr uint32_t kPolyGroups = 0x01;
 constexpr int kSmem = 232448;
 constexpr int kBars = 16 + 16 + 4 + 4 + 8 + 8 + NL + NL + 8;

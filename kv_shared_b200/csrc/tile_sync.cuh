@@ -45,7 +45,8 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
     return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
 }
 
-// Division by a launch's constant (n < 2^31): floor(n / d) = (mulhi(n, m) + n) >> s with
+// Division by a launch's constant (Granlund and Montgomery, "Division by Invariant Integers using
+// Multiplication", 1994; n < 2^31): floor(n / d) = (mulhi(n, m) + n) >> s with
 // s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1.  A division proper is a few hundred
 // cycles of latency to a lone warp.
 struct FastDiv {

@@ -22,7 +22,8 @@ __device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpr
 // fp32 caches on the CUDA cores.  Thread (kp, qt) of 32 x 4 has keys 2 kp, 2 kp + 1 and the PP
 // pairs qt + 4 i of a tile (8; 4 where a sequence has no more than 16), two fp32 FMAs to an
 // instruction.  Bound by the fp32 FMAs and the shared-memory loads between them (10 of 16 bytes to 64
-// FMAs): 16 rows of 16 heads over 16000 keys of 128 52.7 us, a single row over 131072 37.2.
+// FMAs): 16 rows of 16 heads over 16000 keys of 128 52.9 us replayed on the same inputs (55.1 as a call
+// among others), a single row over 131072 37.2.
 template <int D, int PP>
 __global__ void __launch_bounds__(128) accum_f32_kernel(AccumArgs a) {
     constexpr int S_ROWS = 4 * PP;               // (row, head) pairs per tile

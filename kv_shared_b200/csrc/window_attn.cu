@@ -15,8 +15,9 @@
 // n index (a permutation of the output columns, undone on the way out).  Rows are stored with
 // their chunks shifted so that neither read meets a bank twice.  The warps' running (max, sum,
 // O) are joined in shared memory; with few rows and many keys the keys are cut over CTAs as
-// well and a second launch joins the parts in a fixed order.  Measured (16 heads of 128): 32
-// tokens, window 128: 5.7 us; 4 tokens, window 32768, e4m3: 15.1 us (2.3 TB/s).
+// well and a second launch joins the parts in a fixed order.  Measured (16 heads of 128; times in
+// this file are replayed from a graph on the same inputs): 32 tokens, window 128, 5.8 us; 4 tokens,
+// window 32768, e4m3, 15.1 us (2.3 TB/s).  As calls among others on changing inputs: 8.0 and 18.4.
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "internal.h"
@@ -384,9 +385,11 @@ __global__ void __launch_bounds__(NW * 32, 1) window_rows_kernel(WindowArgs a, F
 // the fp32 caches are there for).  Thread (rp, qt) of 32 / RP x 8 has pairs RP rp .. RP rp + RP - 1;
 // keys qt + 8 i of S, dims 4 (qt + 8 j) of O, two fp32 FMAs to an instruction.  RP = 4 makes 8 loads
 // of 16 bytes from shared memory to 64 FMAs and is bound by them and by latency: 2 x 1023 rows of 8
-// heads of 64, window 128, 26.0 us (RP = 2, 12 to 64: 31.4).  RP = 2 has twice the warps, for calls
+// heads of 64, window 128, 25.7 us (RP = 2, 12 to 64: 31.4).  RP = 2 has twice the warps, for calls
 // that leave each SM a CTA at most and are bound by a tile's latency alone, some 2 us: one row of 16
-// heads of 128, window 4096, 14.0 us (RP = 4: 18.5; parts of 256 keys and not of one tile: 37.7).
+// heads of 128, window 4096, 4 sinks, 13.9 us (RP = 4: 18.5; parts of 256 keys: 37.7); without sinks
+// 11.0, for the keys then divide into 128 parts of a tile, where otherwise parts round up to two
+// tiles and half of them have no keys.
 template <int D, int RP>
 __global__ void __launch_bounds__(F_ROWS / RP * F_QT) window_f32_kernel(WindowArgs a) {
     constexpr int NT = F_ROWS / RP * F_QT;
@@ -687,7 +690,7 @@ WindowPlan plan_window(int batch, int n_q, int heads, int kv_dtype, int window, 
     const Shape t = shape(batch, pairs, heads, window, sinks, max_ctx, 256, 1, kMinSplitKeysTile);
     // The tcgen05 kernel is the faster one per key but slow to start and to join, so the small
     // calls are left to the other.  Both estimated, in tenths of a microsecond, from what they
-    // measured (bf16, 16 heads; rows kernel against tile kernel): 64 rows, window 128: 5.9 us
+    // measured (bf16, 16 heads; rows kernel against tile kernel): 64 rows, window 128, 5.9 us
     // against 11.6; 8 x 64 rows: 19.4 against 11.8; 4 x 64 rows, window 1000: 23.6 against 38.5;
     // 256 rows, window 4000: 71 against 41; 8192 rows: 1350 against 120.
     const int64_t cost_r = 40 + r.rounds * (9 * ((r.keys / r.parts + 127) / 128) + 20) + (r.parts > 1 ? 50 : 0);

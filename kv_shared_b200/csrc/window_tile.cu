@@ -19,8 +19,8 @@
 // tensor pipe executes one thread's MMAs in issue order, so P(i) has been read before S(i + 1)
 // overwrites it, and S(i + 1) being complete means that O holds PV(i).  While one half's
 // threads form P the tensor cores work for the other half.  P goes out in two parts, so that PV
-// runs while the rest of the exponentials is formed (the chunk above: 415 us in one part, 390 in
-// four).
+// runs while the rest of the exponentials is formed (8192 rows, window 4096: 353 us in two parts,
+// 415 in one, 390 in four).
 //
 // Work items (sequence, 256 pairs, part of the keys) are dealt to one persistent CTA per SM,
 // and the roles run ahead of one another across items: the next item's Q, K and V are loaded
@@ -36,9 +36,11 @@
 // e4m3 caches: the codes of the rows that the call attends to are first widened to bf16
 // (exact) in the workspace; the rows' scales multiply S and P in fp32.
 //
-// Measured (16 heads of 128, bf16): 8192 rows with a window of 4096 350 us (780 TFLOP/s; 4700
-// cycles a tile of 128 keys, of which the MMAs are 2048 and the exponentials 1800: the chain
-// S, softmax, PV of a half bounds it), 4 x 8192 rows with a window of 128 117 us.
+// Measured (16 heads of 128, bf16, replayed from a graph on the same inputs): 8192 rows with a
+// window of 4096 353 us (780 TFLOP/s; 4700 cycles a tile of 128 keys, of which the MMAs are 2048,
+// the exponentials' unit 1800 and the softmax threads' instructions 3200: the chain S, softmax, PV
+// of a half bounds it), 4 x 8192 rows with a window of 128 117 us.  As calls among others on
+// changing inputs: 355 and 119.
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "internal.h"
@@ -283,6 +285,7 @@ __global__ void __launch_bounds__(NT, 1) window_tile_kernel(const __grid_constan
                             float2 p0 = make_float2(ex2(x0.x), ex2(x0.y)), p1 = make_float2(ex2(x1.x), ex2(x1.y));
                             sum0 = add2(sum0, p0);
                             sum1 = add2(sum1, p1);
+                            // rounded to bf16 for the MMA (2^-8 relative), next to e4m3 rows times the value's scale
                             if (KV8) {
                                 const float4 v4 = *reinterpret_cast<const float4*>(ksc + KT + 32 * i + j);
                                 p0.x *= v4.x; p0.y *= v4.y; p1.x *= v4.z; p1.y *= v4.w;
