@@ -139,7 +139,7 @@ def _stream_here(fn, stream, t):
     or the host's memory is a fault, so one tensor of the call, t, is looked at (all of them would cost a
     single token's call a tenth of its time).  Beside a given stream only another device is refused."""
     if stream is None:
-        if t is not None and t.get_device() != _device():
+        if getattr(t, "get_device", _device)() != _device():
             raise HS2Error(fn, HS2_ERR_INVALID_ARG, "a tensor is not on the current device")
         return _current_stream()
     d = getattr(t, "get_device", lambda: -1)()

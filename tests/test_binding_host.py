@@ -67,3 +67,18 @@ def test_calls_refuse_tensors_of_another_device(name, monkeypatch):
         assert ("current device" in str(e.value)) == refused, (device, stream)
     with pytest.raises(hs.HS2Error):                              # a missing tensor is the library's to refuse
         getattr(hs, name)(*CALLS[name](None), stream=on1)
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_take_what_has_only_an_address(name, monkeypatch):
+    """An object that cannot tell its device passes, with a stream and without."""
+    class Address:
+        def data_ptr(self):
+            return 0x1000
+
+    monkeypatch.setattr(hs, "_device", lambda: 1)
+    monkeypatch.setattr(hs, "_current_stream", lambda: 77)
+    for stream in (None, Stream):
+        with pytest.raises(hs.HS2Error) as e:                      # the library's refusal of the rest
+            getattr(hs, name)(*CALLS[name](Address()), stream=stream)
+        assert e.value.status == hs.HS2_ERR_INVALID_ARG and "current device" not in str(e.value)
