@@ -116,12 +116,13 @@ def _p(t):
 
 
 def _current_stream_getter(c):
-    """A function that gives the current stream's handle: torch's own two calls below
-    torch.cuda.current_stream() where `c` (torch._C) has them (0.1 us against 1), else that."""
+    """A function that gives the current stream's handle (of the current device, d if the caller knows
+    it): torch's own two calls below torch.cuda.current_stream() where `c` (torch._C) has them (0.1 us
+    against 1), else that."""
     raw, device = getattr(c, "_cuda_getCurrentRawStream", None), getattr(c, "_cuda_getDevice", None)
     if raw is None or device is None:
-        return lambda: torch.cuda.current_stream().cuda_stream
-    return lambda: raw(device())
+        return lambda d=None: torch.cuda.current_stream().cuda_stream
+    return lambda d=None: raw(device() if d is None else d)
 
 
 _current_stream = _current_stream_getter(torch._C)
@@ -139,9 +140,13 @@ def _stream_here(fn, stream, t):
     or the host's memory is a fault, so one tensor of the call, t, is looked at (all of them would cost a
     single token's call a tenth of its time).  Beside a given stream only another device is refused."""
     if stream is None:
-        if getattr(t, "get_device", _device)() != _device():
-            raise HS2Error(fn, HS2_ERR_INVALID_ARG, "a tensor is not on the current device")
-        return _current_stream()
+        here = _device()
+        try:
+            if t.get_device() != here:
+                raise HS2Error(fn, HS2_ERR_INVALID_ARG, "a tensor is not on the current device")
+        except AttributeError:                 # None, or an object that has an address alone
+            pass
+        return _current_stream(here)
     d = getattr(t, "get_device", lambda: -1)()
     if d >= 0 and (d != _device() or d != getattr(stream, "device_index", d)):
         raise HS2Error(fn, HS2_ERR_INVALID_ARG, "a tensor or the stream is not on the current device")

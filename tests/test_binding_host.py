@@ -18,11 +18,11 @@ def test_current_stream_without_torchs_private_calls(monkeypatch):
               types.SimpleNamespace(_cuda_getCurrentRawStream=lambda d: 5)):
         assert hs._current_stream_getter(c)() == Stream.cuda_stream
     c = types.SimpleNamespace(_cuda_getDevice=lambda: 3, _cuda_getCurrentRawStream=lambda d: 100 + d)
-    assert hs._current_stream_getter(c)() == 103
+    assert hs._current_stream_getter(c)() == 103 and hs._current_stream_getter(c)(2) == 102
 
 
 def test_streams_given_and_current(monkeypatch):
-    monkeypatch.setattr(hs, "_current_stream", lambda: 77)
+    monkeypatch.setattr(hs, "_current_stream", lambda d=None: 77)
     assert hs._stream() == 77 and hs._stream(Stream) == Stream.cuda_stream
 
 
@@ -57,7 +57,7 @@ def test_calls_refuse_tensors_of_another_device(name, monkeypatch):
     """On device 1: tensors of device 0 and of the host, and a stream of device 0, are refused before the
     library is called; what passes is refused there for its missing arguments (status 1 without a reason)."""
     monkeypatch.setattr(hs, "_device", lambda: 1)
-    monkeypatch.setattr(hs, "_current_stream", lambda: 77)
+    monkeypatch.setattr(hs, "_current_stream", lambda d=None: 77)
     on1, on0 = (types.SimpleNamespace(cuda_stream=5, device_index=i) for i in (1, 0))
     for device, stream, refused in ((0, None, True), (-1, None, True), (1, None, False), (0, on1, True), (1, on0, True),
                                     (1, on1, False), (-1, on1, False), (1, Stream, False), (0, Stream, True)):
@@ -77,7 +77,7 @@ def test_calls_take_what_has_only_an_address(name, monkeypatch):
             return 0x1000
 
     monkeypatch.setattr(hs, "_device", lambda: 1)
-    monkeypatch.setattr(hs, "_current_stream", lambda: 77)
+    monkeypatch.setattr(hs, "_current_stream", lambda d=None: 77)
     for stream in (None, Stream):
         with pytest.raises(hs.HS2Error) as e:                      # the library's refusal of the rest
             getattr(hs, name)(*CALLS[name](Address()), stream=stream)
